@@ -70,9 +70,11 @@ typedef enum {
 typedef enum {
   TS_F32 = 0,       /* fp32 states, weights and arithmetic (SIMT kernels)              */
   TS_BF16 = 1,      /* bf16 states/weights, fp32 accumulation (tcgen05 kind::f16)      */
-  TS_FP8_E4M3 = 2   /* bf16 states, e4m3 GEMM operands (tcgen05 kind::f8f6f4), bf16
+  TS_FP8_E4M3 = 2,  /* bf16 states, e4m3 GEMM operands (tcgen05 kind::f8f6f4), bf16
                        attention; weights quantised per output channel, activations
                        per token ([TileShare] Tab. S2 "FP8")                          */
+  TS_INT8 = 3       /* as TS_FP8_E4M3 with signed 8-bit integer GEMM operands and exact
+                       int32 sums (tcgen05 kind::i8); see ts_quantize_rows_i8          */
 } ts_dtype;
 
 /* Block flavour ([TileShare] Tab. S1 block; Tab. S6 profiles a block with "RMSNorm +
@@ -124,8 +126,9 @@ typedef struct {
 
 /* One layer's parameters, all device pointers.  Matrices are [out, in] row-major
    (y = x W^T + b).  Matrix element type: float for TS_F32, bf16 for TS_BF16, e4m3
-   bytes for TS_FP8_E4M3 (then s_* hold the per-output-channel fp32 scales, see
-   ts_quantize_rows_e4m3).  Vectors are always fp32. */
+   bytes for TS_FP8_E4M3 and signed bytes for TS_INT8 (then s_* hold the
+   per-output-channel fp32 scales, see ts_quantize_rows_e4m3 and
+   ts_quantize_rows_i8).  Vectors are always fp32. */
 typedef struct {
   const float* ln1_g; const float* ln1_b;    /* [d]                 */
   const void* w_qkv;  const float* b_qkv;    /* [3d, d], [3d]; rows: q | k | v, head h at h*hd */
@@ -134,8 +137,8 @@ typedef struct {
   const float* ln2_g; const float* ln2_b;    /* [d]                 */
   const void* w_1;    const float* b_1;      /* [f, d], [f]; [2f, d], [2f] for TS_BLOCK_RMS_SWIGLU */
   const void* w_2;    const float* b_2;      /* [d, f], [d]          */
-  const float* s_qkv; const float* s_o;      /* TS_FP8_E4M3 only: [3d], [d] */
-  const float* s_1;   const float* s_2;      /* TS_FP8_E4M3 only: [f] ([2f] SwiGLU), [d] */
+  const float* s_qkv; const float* s_o;      /* 8-bit dtypes only: [3d], [d] */
+  const float* s_1;   const float* s_2;      /* 8-bit dtypes only: [f] ([2f] SwiGLU), [d] */
 } ts_layer_weights;
 
 /* ---------------------------------------------------------------------------
@@ -188,6 +191,34 @@ ts_status ts_block_tiled(ts_plan_t plan, const ts_model_desc* model, const ts_la
    (the only approximate step); each register keeps its own tile's output. */
 ts_status ts_block_shared(ts_plan_t plan, const ts_model_desc* model, const ts_layer_weights* w,
                           void* S, void* workspace, size_t workspace_bytes, void* stream);
+
+/* What a sandwich layer adds to a layer's weights: a norm after each half (attention
+   with its out-projection, MLP), a gate and a residual scale.  All device pointers,
+   16-byte aligned, any of them NULL for none; groups and row_group serve both gates. */
+typedef struct {
+  const float* post1_g; const float* post1_b;  /* [d] norm after the out-projection; the bias for LayerNorm only */
+  const float* gate1;   const float* scale1;   /* [groups, d], [d]                  */
+  const float* post2_g; const float* post2_b;  /* [d] norm after the MLP            */
+  const float* gate2;   const float* scale2;   /* [groups, d], [d]                  */
+  const int* row_group; /* [rows of the state] gate row of each state row, in [0, groups);
+                           NULL: gate row 0 for all (see ts_norm_gate)               */
+  int groups;
+} ts_sandwich_weights;
+
+/* ts_block_shared and ts_block_tiled with norms on both sides of each half, a gate (for
+   decoders conditioned per frame or per image) and a residual scale:
+     x = x + gate1 * scale1 * Norm_post1(out-projection(...Norm1(x)))
+     x = x + gate2 * scale2 * Norm_post2(MLP(Norm2(x)))
+   The norms are those of the model's block flavour.  In place on S [U + T*R, d] or
+   X [T, N, d].  With neither norm, gate nor scale the function is that of ts_block_shared
+   or ts_block_tiled, up to one rounding of each half's output to the model dtype.
+   Workspace as for ts_block_shared. */
+ts_status ts_block_shared_sandwich(ts_plan_t plan, const ts_model_desc* model, const ts_layer_weights* w,
+                                   const ts_sandwich_weights* sw, void* S, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+ts_status ts_block_tiled_sandwich(ts_plan_t plan, const ts_model_desc* model, const ts_layer_weights* w,
+                                  const ts_sandwich_weights* sw, void* X, void* workspace,
+                                  size_t workspace_bytes, void* stream);
 
 /* Shared layer without a caller workspace.  The paper has no counterpart: this
    entry point exists for callers that cannot allocate device memory, such as a
@@ -248,6 +279,17 @@ ts_status ts_gather_tiles(ts_plan_t plan, const ts_model_desc* model, const void
    matrices (per output channel) before calling the layers. */
 ts_status ts_quantize_rows_e4m3(const void* x, int rows, int cols, void* q, float* scale,
                                 void* stream);
+
+/* Per-row quantisation to signed 8-bit integers used by TS_INT8.  With a = max|x[r, :]|:
+     scale[r] = a / 127,  inv = 127 / a  (each rounded to fp32),
+     q[r, c]  = x[r, c] * inv rounded once to the nearest integer, ties to even
+   so that x is about q * scale and q lies in [-127, 127].  A row with a < 2^-100 counts
+   as zero (scale 1, q 0).  A row that holds an infinity or a NaN gets q 0 and a NaN
+   scale, so that every product with it is NaN.
+   x bf16 [rows, cols] (device), q signed bytes [rows, cols] (device), scale fp32 [rows]
+   (device); cols % 8 == 0.  Used once on the weight matrices (per output channel). */
+ts_status ts_quantize_rows_i8(const void* x, int rows, int cols, void* q, float* scale,
+                              void* stream);
 
 /* Operations a partially shared layer runs once per token (bit mask). */
 typedef enum {

@@ -33,23 +33,57 @@ typedef enum {
    y[r] = (x[r] - mean) / sqrt(var + eps) * g + b, population variance, eps = eps_ln.
    For TS_BLOCK_RMS_SWIGLU models RMSNorm instead: y[r] = x[r] / sqrt(mean(x[r]^2) +
    eps) * g, and b is unused (may be NULL).
-   x, y [rows, d] in the model dtype (bf16 for TS_FP8_E4M3); g, b fp32 [d]. */
+   x, y [rows, d] in the model dtype (bf16 for the 8-bit dtypes); g, b fp32 [d]. */
 ts_status ts_op_layernorm(const ts_model_desc* model, const void* x, int rows,
                           const float* g, const float* b, void* y, void* stream);
 
+/* Norms before and after a block, its gate and its residual scale.  All device pointers,
+   vectors 16-byte aligned. */
+typedef struct {
+  const float* post_g; const float* post_b; /* [d] norm of the block's output; post_g NULL: none   */
+  const float* pre_g;  const float* pre_b;  /* [d] norm before the next block; pre_g NULL: none    */
+  const float* gate;                        /* [groups, d]; NULL: 1                                */
+  const float* scale;                       /* [d] residual scale; NULL: 1                         */
+  int groups;                               /* rows of the gate (>= 1 with a gate)                 */
+} ts_norm_gate;
+
+/* The seam between two blocks in one pass over the residual stream:
+     x_out[r] = x[r] + gate[row_group[r]] * scale * Norm_post(y[r])
+     xn[r]    = Norm_pre(x_out[r])           (x_out before it is rounded)
+   Both norms as in ts_op_layernorm (biases are unused by RMSNorm and may be NULL).
+   row_group [rows] int32 holds each row's gate row; NULL: gate row 0 (unused without a gate).
+   x, y, x_out [rows, d] in the model dtype (bf16 for the 8-bit dtypes); x_out may be x.
+   xn [rows, d] likewise, or, with xn_scale [rows] set (8-bit dtypes only), 8-bit rows with
+   their scales as ts_quantize_rows_* would give them, for ts_op_linear_q8; xn must be
+   NULL where pre_g is.  No other overlap of the buffers is allowed.
+   A row_group entry outside [0, groups) sets the device status (TS_ERR_DEVICE_CHECK, see
+   ts_device_status) and leaves that row's outputs as they were. */
+ts_status ts_op_norm_gate(const ts_model_desc* model, const ts_norm_gate* p, const void* x,
+                          const void* y, const int* row_group, int rows, void* x_out,
+                          void* xn, float* xn_scale, void* stream);
+
 /* Linear layer y = x W^T + b with a fused epilogue ([TileShare] Fig. 2: QKV,
    out-projection and MLP once per token).  x [rows, K], W [N, K], y [rows, N], in
-   the model dtype (TS_FP8_E4M3: x bf16, W e4m3 with per-row scales w_scale [N];
+   the model dtype (8-bit dtypes: x and y bf16, W 8-bit with per-row scales w_scale [N];
    x is quantised per row inside the call using `scratch`, which must hold
    rows * K + 4 * rows bytes; scratch is unused otherwise and may be NULL).
-   bf16/e4m3 need K % 64 == 0 and N % 64 == 0 (K % 128 for e4m3). */
+   bf16/e4m3 need K % 64 == 0 and N % 64 == 0 (K % 128 for e4m3); int8 needs
+   K % 16 == 0, N % 8 == 0 and K <= 131056. */
 ts_status ts_op_linear(const ts_model_desc* model, const void* x, int rows, int K,
                        const void* W, const float* w_scale, int N, const float* bias,
                        ts_epilogue epi, void* y, void* scratch, void* stream);
 
+/* The same linear layer of rows that are 8-bit already (8-bit dtypes only): x [rows, K]
+   e4m3 or signed bytes with x_scale [rows], as ts_quantize_rows_* and ts_op_norm_gate
+   write them; y = epi((x W^T) * x_scale * w_scale + b), y bf16 [rows, N].  Integer sums
+   are exact.  x may hold -128.  Sizes as for ts_op_linear. */
+ts_status ts_op_linear_q8(const ts_model_desc* model, const void* x, const float* x_scale,
+                          int rows, int K, const void* W, const float* w_scale, int N,
+                          const float* bias, ts_epilogue epi, void* y, void* stream);
+
 /* Norm1 + QKV projection + QK-RMSNorm + RoPE of the rows of a state ([TileShare]
    Tab. S1: Norm1, QKV, QK-RMSNorm once per token; RoPE on tile coordinates).
-   state [rows, d] -> qkv [rows, 3d] (model dtype; bf16 for TS_FP8_E4M3).
+   state [rows, d] -> qkv [rows, 3d] (model dtype; bf16 for the 8-bit dtypes).
    TS_ROWS_TILED rotates q and k of slot j of every tile by its tile-local
    coordinates and leaves rows 0 .. R-1 (the registers) unrotated.  TS_ROWS_SHARED
    rotates grid token u by its grid coordinates and the registers of tile t by

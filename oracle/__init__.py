@@ -20,6 +20,7 @@ Modules
     plan    tiling of the token grid, tile<->token index maps, blend weights w-bar
     layers  per-tile layer, shared layer, merge, TileShare-k stack
     fp8     OCP FP8 E4M3 rounding and the per-channel / per-token scaled GEMM
+    int8    signed 8-bit integer rows and the per-channel / per-token scaled GEMM
     flops   analytic FLOP count of a tiled and a shared layer
 
 Parity status: every function here is pinned by ``tests/test_oracle_*.py``
@@ -27,4 +28,4 @@ against closed forms, brute force, library routines and the exactness
 statements of the pages; see the header of each module.
 """
 
-from . import plan, layers, fp8, flops  # noqa: F401
+from . import plan, layers, fp8, int8, flops  # noqa: F401

@@ -58,6 +58,7 @@ import numpy as np
 from scipy.special import erf
 
 from . import fp8 as _fp8
+from . import int8 as _int8
 
 
 @dataclass(frozen=True)
@@ -70,6 +71,7 @@ class Model:
     eps_qk: float = 1e-6
     rope_base: float = 10000.0
     fp8: bool = False         # e4m3 GEMMs with per-channel / per-token scales
+    int8: bool = False        # signed 8-bit integer GEMMs, scales likewise
     block: str = "ln_gelu"    # "ln_gelu" (R4) or "rms_swiglu" (R13)
 
     @property
@@ -128,9 +130,12 @@ def rope(x, pos, m: Model):
 
 
 def linear(x, w, b, m: Model):
-    """x @ w.T + b; with m.fp8 the product is the e4m3 scaled GEMM of fp8.scaled_matmul."""
+    """x @ w.T + b; with m.fp8 the product is the e4m3 scaled GEMM of fp8.scaled_matmul, with
+    m.int8 the integer one of int8.scaled_matmul."""
     if m.fp8:
         y = _fp8.scaled_matmul(x, w)
+    elif m.int8:
+        y = _int8.scaled_matmul(x, w)
     else:
         y = x @ w.T
     return y + b
@@ -275,6 +280,48 @@ def block_shared(S, p, m: Model, plan):
     A = merge(O, plan)
     S = S + linear(A, p["w_o"], p["b_o"], m)
     return mlp_residual(S, p, m)
+
+
+def norm_gate(x, y, m: Model, post_g=None, post_b=None, gate=None, scale=None, row_group=None, pre_g=None,
+              pre_b=None):
+    """(x', xn): x' = x + gate[row_group] * scale * Norm_post(y), xn = Norm_pre(x') (None without pre_g).
+
+    Either norm is the block's; what is None drops out (no norm, a factor of 1, group 0)."""
+    if post_g is not None:
+        y = block_norm(y, post_g, post_b, m)
+    k = np.ones(x.shape[-1])
+    if gate is not None:
+        k = gate[np.zeros(len(x), np.int64) if row_group is None else row_group]
+    if scale is not None:
+        k = k * scale
+    x = x + k * y
+    return x, (None if pre_g is None else block_norm(x, pre_g, pre_b, m))
+
+
+def _sandwich(x, att, p, sw, m: Model):
+    """Both halves of a sandwich layer on rows x with attention outputs att (before the out-projection)."""
+    x, h = norm_gate(x, linear(att, p["w_o"], p["b_o"], m), m, sw.get("post1_g"), sw.get("post1_b"), sw.get("gate1"),
+                     sw.get("scale1"), sw.get("row_group"), p["ln2_g"], p["ln2_b"])
+    a = linear(h, p["w_1"], p["b_1"], m)
+    h = silu(a[:, :m.mlp]) * a[:, m.mlp:] if m.block == "rms_swiglu" else gelu(a)
+    return norm_gate(x, linear(h, p["w_2"], p["b_2"], m), m, sw.get("post2_g"), sw.get("post2_b"), sw.get("gate2"),
+                     sw.get("scale2"), sw.get("row_group"))[0]
+
+
+def block_shared_sandwich(S, p, sw, m: Model, plan):
+    """A shared layer on S [U + T*R, d] whose halves' outputs pass a norm, a gate and a scale (dict sw)."""
+    S = S.astype(np.float64)
+    return _sandwich(S, merge(shared_attention_outputs(S, p, m, plan), plan), p, sw, m)
+
+
+def block_tiled_sandwich(X, p, sw, m: Model, plan):
+    """The same layer per tile on X [T, N, d]; row_group runs over the T * N rows."""
+    T, N = plan.T, plan.N
+    O = np.empty((T, N, m.d), dtype=np.float64)
+    for t in range(T):
+        q, k, v = qkv_project(X[t].astype(np.float64), p, m)
+        O[t] = tile_attention(q, k, v, plan.slot_pos, m)
+    return _sandwich(X.reshape(T * N, -1).astype(np.float64), O.reshape(T * N, -1), p, sw, m).reshape(X.shape)
 
 
 SHARED_OPS = ("qkv", "out", "mlp")

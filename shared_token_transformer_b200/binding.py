@@ -22,12 +22,12 @@ TS_OK = 0
 TS_BLEND_LINEAR_RAMP = 0
 TS_BLEND_HARD_STITCH = 1
 TS_SHARE_QKV, TS_SHARE_OUT, TS_SHARE_MLP = 1, 2, 4
-TS_F32, TS_BF16, TS_FP8_E4M3 = 0, 1, 2
+TS_F32, TS_BF16, TS_FP8_E4M3, TS_INT8 = 0, 1, 2, 3
 TS_ROWS_SHARED, TS_ROWS_TILED = 0, 1
 TS_EPI_BIAS, TS_EPI_BIAS_GELU, TS_EPI_BIAS_RESID, TS_EPI_BIAS_SWIGLU = 0, 1, 2, 3
 TS_BLOCK_LN_GELU, TS_BLOCK_RMS_SWIGLU = 0, 1
 BLOCKS = {"ln_gelu": TS_BLOCK_LN_GELU, "rms_swiglu": TS_BLOCK_RMS_SWIGLU}
-DTYPES = {"f32": TS_F32, "bf16": TS_BF16, "fp8": TS_FP8_E4M3}
+DTYPES = {"f32": TS_F32, "bf16": TS_BF16, "fp8": TS_FP8_E4M3, "int8": TS_INT8}
 
 _int3 = ctypes.c_int * 3
 _cp = ctypes.c_void_p
@@ -56,6 +56,16 @@ _WEIGHT_FIELDS = ["ln1_g", "ln1_b", "w_qkv", "b_qkv", "q_g", "k_g", "w_o", "b_o"
 
 class LayerWeights(ctypes.Structure):
     _fields_ = [(n, _cp) for n in _WEIGHT_FIELDS]
+
+
+class SandwichWeights(ctypes.Structure):
+    _fields_ = [(n, _cp) for n in ("post1_g", "post1_b", "gate1", "scale1", "post2_g", "post2_b", "gate2", "scale2",
+                                   "row_group")] + [("groups", ctypes.c_int)]
+
+
+class NormGate(ctypes.Structure):
+    _fields_ = [(n, _cp) for n in ("post_g", "post_b", "pre_g", "pre_b", "gate", "scale")] + \
+        [("groups", ctypes.c_int)]
 
 
 class TraceEntry(ctypes.Structure):
@@ -91,6 +101,7 @@ _SIGS = {
     "ts_decode_stack": [_cp, ctypes.POINTER(ModelDesc), ctypes.POINTER(LayerWeights), ctypes.c_int, ctypes.c_int,
                         _cp, _cp, _cp, _cp, ctypes.c_size_t, _cp],
     "ts_quantize_rows_e4m3": [_cp, ctypes.c_int, ctypes.c_int, _cp, _cp, _cp],
+    "ts_quantize_rows_i8": [_cp, ctypes.c_int, ctypes.c_int, _cp, _cp, _cp],
     "ts_gather_tiles": [_cp, ctypes.POINTER(ModelDesc), _cp, _cp, _cp, _cp],
     "ts_trace_begin": [ctypes.c_int],
     "ts_trace_end": [ctypes.POINTER(TraceEntry), ctypes.c_int, ctypes.POINTER(ctypes.c_int)],
@@ -99,9 +110,17 @@ _SIGS = {
     "ts_selftest_bounded_wait": [ctypes.c_longlong, _cp, _cp],
     "ts_status_string": [ctypes.c_int],
     "ts_last_error": [],
+    "ts_block_shared_sandwich": [_cp, ctypes.POINTER(ModelDesc), ctypes.POINTER(LayerWeights),
+                                 ctypes.POINTER(SandwichWeights), _cp, _cp, ctypes.c_size_t, _cp],
+    "ts_block_tiled_sandwich": [_cp, ctypes.POINTER(ModelDesc), ctypes.POINTER(LayerWeights),
+                                ctypes.POINTER(SandwichWeights), _cp, _cp, ctypes.c_size_t, _cp],
+    "ts_op_norm_gate": [ctypes.POINTER(ModelDesc), ctypes.POINTER(NormGate), _cp, _cp, _cp, ctypes.c_int, _cp, _cp,
+                        _cp, _cp],
     "ts_op_layernorm": [ctypes.POINTER(ModelDesc), _cp, ctypes.c_int, _cp, _cp, _cp, _cp],
     "ts_op_linear": [ctypes.POINTER(ModelDesc), _cp, ctypes.c_int, ctypes.c_int, _cp, _cp, ctypes.c_int, _cp,
                      ctypes.c_int, _cp, _cp, _cp],
+    "ts_op_linear_q8": [ctypes.POINTER(ModelDesc), _cp, _cp, ctypes.c_int, ctypes.c_int, _cp, _cp, ctypes.c_int, _cp,
+                        ctypes.c_int, _cp, _cp],
     "ts_op_qkv": [_cp, ctypes.POINTER(ModelDesc), ctypes.POINTER(LayerWeights), ctypes.c_int, _cp, _cp, _cp, _cp],
     "ts_op_attention": [_cp, ctypes.POINTER(ModelDesc), ctypes.c_int, _cp, _cp, _cp],
     "ts_op_merge": [_cp, ctypes.POINTER(ModelDesc), _cp, ctypes.c_int, _cp, _cp],
@@ -206,6 +225,32 @@ def layer_weights(tensors):
     return w
 
 
+def _keep(struct, tensors):
+    for n, t in tensors.items():
+        if t is not None:
+            setattr(struct, n, t.data_ptr())
+    gates = [t for n, t in tensors.items() if n.startswith("gate") and t is not None]
+    if len({t.shape[0] for t in gates}) > 1:
+        raise ValueError("the gates have different numbers of groups")
+    struct.groups = gates[0].shape[0] if gates else 0
+    struct._tensors = dict(tensors)
+    return struct
+
+
+def norm_gate_desc(post_g=None, post_b=None, pre_g=None, pre_b=None, gate=None, scale=None):
+    """ts_norm_gate of device tensors (fp32; gate [groups, d]), kept alive by the struct."""
+    return _keep(NormGate(), {"post_g": post_g, "post_b": post_b, "pre_g": pre_g, "pre_b": pre_b, "gate": gate,
+                              "scale": scale})
+
+
+def sandwich_weights(post1_g=None, post1_b=None, gate1=None, scale1=None, post2_g=None, post2_b=None, gate2=None,
+                     scale2=None, row_group=None):
+    """ts_sandwich_weights of device tensors (fp32, as norm_gate_desc, for both halves of a layer; row_group int32)."""
+    return _keep(SandwichWeights(), {"post1_g": post1_g, "post1_b": post1_b, "gate1": gate1, "scale1": scale1,
+                                     "post2_g": post2_g, "post2_b": post2_b, "gate2": gate2, "scale2": scale2,
+                                     "row_group": row_group})
+
+
 def workspace_size(plan, model, L=0, k=0):
     n = ctypes.c_size_t()
     _check("ts_workspace_size", lib().ts_workspace_size(plan.handle, ctypes.byref(model), L, k, ctypes.byref(n)))
@@ -230,6 +275,20 @@ def block_partial(plan, model, weights, shared_ops, X, ws, stream=None):
     _check("ts_block_partial", lib().ts_block_partial(plan.handle, ctypes.byref(model), ctypes.byref(weights),
                                                       int(shared_ops), _ptr(X), _ptr(ws),
                                                       ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def block_shared_sandwich(plan, model, weights, sandwich, S, ws, stream=None):
+    _check("ts_block_shared_sandwich",
+           lib().ts_block_shared_sandwich(plan.handle, ctypes.byref(model), ctypes.byref(weights),
+                                          ctypes.byref(sandwich), _ptr(S), _ptr(ws),
+                                          ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def block_tiled_sandwich(plan, model, weights, sandwich, X, ws, stream=None):
+    _check("ts_block_tiled_sandwich",
+           lib().ts_block_tiled_sandwich(plan.handle, ctypes.byref(model), ctypes.byref(weights),
+                                         ctypes.byref(sandwich), _ptr(X), _ptr(ws),
+                                         ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def block_shared_noalloc(plan, model, weights, S, stream=None):
@@ -275,6 +334,12 @@ def quantize_rows_e4m3(x, q, scale, stream=None):
                                                                 _stream(stream)))
 
 
+def quantize_rows_i8(x, q, scale, stream=None):
+    rows, cols = x.shape
+    _check("ts_quantize_rows_i8", lib().ts_quantize_rows_i8(_ptr(x), rows, cols, _ptr(q), _ptr(scale),
+                                                            _stream(stream)))
+
+
 def device_status():
     _check("ts_device_status", lib().ts_device_status())
 
@@ -289,11 +354,26 @@ def op_layernorm(model, x, g, b, y, stream=None):
                                                     _ptr(y), _stream(stream)))
 
 
+def op_norm_gate(model, gates, x, y, x_out, xn=None, xn_scale=None, row_group=None, stream=None):
+    """ts_op_norm_gate: x_out = x + gate * scale * Norm_post(y), xn = Norm_pre(x_out); with xn_scale, xn is 8-bit rows."""
+    _check("ts_op_norm_gate", lib().ts_op_norm_gate(ctypes.byref(model), ctypes.byref(gates), _ptr(x), _ptr(y),
+                                                    _ptr(row_group), x.shape[0], _ptr(x_out), _ptr(xn),
+                                                    _ptr(xn_scale), _stream(stream)))
+
+
 def op_linear(model, x, W, bias, y, epi=TS_EPI_BIAS, w_scale=None, scratch=None, stream=None):
     rows, K = x.shape
     N = W.shape[0] // 2 if epi == TS_EPI_BIAS_SWIGLU else W.shape[0]     # output width
     _check("ts_op_linear", lib().ts_op_linear(ctypes.byref(model), _ptr(x), rows, K, _ptr(W), _ptr(w_scale), N,
                                               _ptr(bias), epi, _ptr(y), _ptr(scratch), _stream(stream)))
+
+
+def op_linear_q8(model, x, x_scale, W, w_scale, bias, y, epi=TS_EPI_BIAS, stream=None):
+    """ts_op_linear_q8: the linear layer of rows that are 8-bit already, with their scales."""
+    rows, K = x.shape
+    N = W.shape[0] // 2 if epi == TS_EPI_BIAS_SWIGLU else W.shape[0]     # output width
+    _check("ts_op_linear_q8", lib().ts_op_linear_q8(ctypes.byref(model), _ptr(x), _ptr(x_scale), rows, K, _ptr(W),
+                                                    _ptr(w_scale), N, _ptr(bias), epi, _ptr(y), _stream(stream)))
 
 
 def op_qkv(plan, model, weights, mode, state, qkv, scratch, stream=None):

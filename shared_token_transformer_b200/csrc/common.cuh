@@ -255,6 +255,26 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
+// Same with signed 8-bit integer operands and int32 accumulation (exact).
+__device__ __forceinline__ void tc_mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_i8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // 32 consecutive fp32 columns of this thread's TMEM lane (lane quarter = warp % 4).
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   uint32_t r[32];
@@ -291,9 +311,9 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr) {
 
 // Instruction descriptor: fp32 accumulator, A and B K-major, M = m (128, or 256
 // for a two-SM pair), N = n.  a/b format: bf16 = 1 for kind::f16, e4m3 = 0 for
-// kind::f8f6f4.
-__host__ __device__ constexpr uint32_t idesc_make(uint32_t ab_format, int n, int m = 128) {
-  return (1u << 4)                                // D format: f32
+// kind::f8f6f4, signed 8-bit = 1 for kind::i8.  d format: f32 = 1, s32 = 2 (kind::i8).
+__host__ __device__ constexpr uint32_t idesc_make(uint32_t ab_format, int n, int m = 128, uint32_t d_format = 1) {
+  return (d_format << 4)                          // D format
          | (ab_format << 7) | (ab_format << 10)   // A, B format
          | (static_cast<uint32_t>(n >> 3) << 17)  // N / 8
          | (static_cast<uint32_t>(m >> 4) << 24);    // M / 16
@@ -463,6 +483,49 @@ __device__ __forceinline__ void rope_table_fill(const RopeTable& rt, int e) {
 __device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float a, float b) {
   return static_cast<uint16_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
 }
+
+// ----------------------------------------------------------------------------
+// rows as signed 8-bit integers: one fp32 scale per row, q = nearest integer to
+// x * inv (ties to even), inv = 127 / max|x| and scale = max|x| / 127 rounded to fp32
+// ----------------------------------------------------------------------------
+struct RowQuantS8 {
+  float inv, scale;
+  uint32_t keep;   // all ones, or 0 for a row that is not finite
+};
+// From the bits of the row's largest magnitude (NaN bits exceed infinity's, so a
+// maximum over bits keeps a NaN).  Rows below 2^-100 count as zero (their reciprocal
+// would leave the range of fp32); a row with an infinity or a NaN gets q = 0 and a NaN
+// scale, so that whatever is computed from it is NaN.
+__device__ __forceinline__ RowQuantS8 row_quant_s8(uint32_t amax_bits) {
+  const float a = __uint_as_float(amax_bits);
+  RowQuantS8 r;
+  if (amax_bits >= 0x7f800000u) {
+    r.inv = 0.f;
+    r.scale = __uint_as_float(0x7fffffffu);
+    r.keep = 0u;
+  } else if (a < 7.8886090522101181e-31f) {
+    r.inv = 0.f;
+    r.scale = 1.f;
+    r.keep = 0xffffffffu;
+  } else {
+    r.inv = __fdiv_rn(127.f, a);
+    r.scale = __fdiv_rn(a, 127.f);
+    r.keep = 0xffffffffu;
+  }
+  return r;
+}
+// Four integers as bytes (low = first).  x * inv + 1.5 * 2^23 is rounded once, at the
+// integers, and its low byte is the integer in two's complement (|x * inv| <= 127).
+__device__ __forceinline__ uint32_t quant_s8x4(float a, float b, float c, float d, const RowQuantS8& r) {
+  const uint64_t inv2 = splat_f32x2(r.inv), magic = splat_f32x2(12582912.f);
+  const uint64_t t0 = fma_f32x2(pack_f32x2(a, b), inv2, magic);
+  const uint64_t t1 = fma_f32x2(pack_f32x2(c, d), inv2, magic);
+  const uint32_t w0 = __byte_perm(static_cast<uint32_t>(t0), static_cast<uint32_t>(t0 >> 32), 0x0040);
+  const uint32_t w1 = __byte_perm(static_cast<uint32_t>(t1), static_cast<uint32_t>(t1 >> 32), 0x0040);
+  return __byte_perm(w0, w1, 0x5410) & r.keep;
+}
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+__device__ __forceinline__ uint32_t warp_max_u32(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
 
 // Rotation angle pos * theta with theta given as a float pair (hi + lo): the
 // product is split into a rounded part and its exact error so that the cosine

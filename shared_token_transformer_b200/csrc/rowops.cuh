@@ -29,14 +29,35 @@ struct Vec<float> {
 };
 
 // Write one row held by a warp (NV vectors of E elements per lane, lane-strided) in
-// the output format: T (bf16 / fp32), or e4m3 bytes + per-row scale absmax / 448.
-template <typename T, int NV, bool Q8>
+// the output format: T (bf16 / fp32), or e4m3 bytes + per-row scale absmax / 448, or
+// signed 8-bit integers + per-row scale absmax / 127.
+enum RowFormat : int { ROW_T = 0, ROW_E4M3 = 1, ROW_S8 = 2 };
+template <typename T, int NV, int Q8>
 __device__ __forceinline__ void store_row(const float (&v)[NV][Vec<T>::E], int lane, T* out, uint8_t* q8,
                                           float* qscale, size_t row, int d) {
   constexpr int E = Vec<T>::E;
-  if (!Q8) {
+  if (Q8 == ROW_T) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) Vec<T>::store(out + row * d + (i * 32 + lane) * E, v[i]);
+  } else if (Q8 == ROW_S8) {
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e) amax = max(amax, abs_bits(v[i][e]));
+    const RowQuantS8 r = row_quant_s8(warp_max_u32(amax));
+    if (lane == 0) qscale[row] = r.scale;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      uint32_t w[E / 4];
+#pragma unroll
+      for (int e = 0; e < E; e += 4) w[e / 4] = quant_s8x4(v[i][e], v[i][e + 1], v[i][e + 2], v[i][e + 3], r);
+      uint8_t* dst = q8 + row * d + (i * 32 + lane) * E;
+      if (E == 8)
+        *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(w);
+      else
+        *reinterpret_cast<uint32_t*>(dst) = w[0];
+    }
   } else {
     float amax = 0.f;
 #pragma unroll
@@ -70,7 +91,7 @@ __device__ __forceinline__ void store_row(const float (&v)[NV][Vec<T>::E], int l
 // time, the warp's next row loaded before the current one is normalised, so two
 // rows per warp are in flight); blocks past them (when rt.cs is set) fill the RoPE
 // table that the next QKV GEMM reads.
-template <typename T, int NV, bool Q8>
+template <typename T, int NV, int Q8>
 __global__ void __launch_bounds__(256) layernorm_kernel(const T* __restrict__ x, int rows, int d,
                                                         const float* __restrict__ g, const float* __restrict__ b,
                                                         float eps, int rms, T* __restrict__ y, uint8_t* __restrict__ q8,
@@ -156,12 +177,159 @@ __global__ void __launch_bounds__(256) layernorm_generic_kernel(const T* __restr
 }
 
 // ---------------------------------------------------------------------------
+// The seam between two halves of a block, one pass over the residual stream:
+//   x' = x + gate[group(r)] * scale * Norm_post(y),   xn = Norm_pre(x')
+// with either norm, the gate and the scale optional.  Both norms are LayerNorm
+// (population variance, two passes over the row in registers) or, with rms set,
+// RMSNorm.  x' enters the second norm unrounded.  One warp per row.
+// ---------------------------------------------------------------------------
+struct NormGateArgs {
+  int rows, d, groups, rms;
+  float eps;
+  const float* post_g;     // [d] or null: y enters as it is
+  const float* post_b;     // [d], LayerNorm only
+  const float* pre_g;      // [d] or null: xn is not written
+  const float* pre_b;      // [d], LayerNorm only
+  const float* gate;       // [groups, d] or null: 1
+  const float* scale;      // [d] or null: 1
+  const int* row_group;    // [rows] or null: group 0
+};
+
+// group of a row; a number outside [0, groups) sets the device status and gives -1,
+// and the row's outputs are left as they are
+__device__ __forceinline__ int norm_gate_group(const NormGateArgs& a, size_t row) {
+  if (!a.row_group) return 0;
+  const int g = a.row_group[row];
+  if (static_cast<unsigned>(g) >= static_cast<unsigned>(a.groups)) {
+    set_status(kStatusDeviceCheck);
+    return -1;
+  }
+  return g;
+}
+
+// normalise a row held by a warp in place: (v - mean) * rstd * g + b
+template <typename T, int NV>
+__device__ __forceinline__ void norm_row(float (&v)[NV][Vec<T>::E], int lane, int d, const float* g, const float* b,
+                                         float eps, int rms) {
+  constexpr int E = Vec<T>::E;
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < E; ++e) s += v[i][e];
+  const float mean = rms ? 0.f : warp_sum(s) / d;
+  float q = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float c = v[i][e] - mean;
+      q = fmaf(c, c, q);
+    }
+  const float rstd = rsqrtf(warp_sum(q) / d + eps);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c0 = (i * 32 + lane) * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 4) {
+      const float4 gg = __ldg(reinterpret_cast<const float4*>(g + c0 + e));
+      const float4 bb = rms ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldg(reinterpret_cast<const float4*>(b + c0 + e));
+      v[i][e] = (v[i][e] - mean) * rstd * gg.x + bb.x;
+      v[i][e + 1] = (v[i][e + 1] - mean) * rstd * gg.y + bb.y;
+      v[i][e + 2] = (v[i][e + 2] - mean) * rstd * gg.z + bb.z;
+      v[i][e + 3] = (v[i][e + 3] - mean) * rstd * gg.w + bb.w;
+    }
+  }
+}
+
+template <typename T, int NV, int Q8>
+__global__ void __launch_bounds__(256) norm_gate_kernel(const T* x, const T* y, T* x_out, T* xn, uint8_t* q8,
+                                                        float* qscale, const NormGateArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int E = Vec<T>::E;
+  const int lane = threadIdx.x & 31;
+  const size_t step = static_cast<size_t>(gridDim.x) * (blockDim.x >> 5);
+  for (size_t row = static_cast<size_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+       row < static_cast<size_t>(a.rows); row += step) {
+    const int group = norm_gate_group(a, row);
+    if (group < 0) continue;
+    float v[NV][E];
+    uint4 raw[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) raw[i] = *reinterpret_cast<const uint4*>(x + row * a.d + (i * 32 + lane) * E);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) Vec<T>::load(y + row * a.d + (i * 32 + lane) * E, v[i]);
+    if (a.post_g) norm_row<T, NV>(v, lane, a.d, a.post_g, a.post_b, a.eps, a.rms);
+    const float* gate = a.gate ? a.gate + static_cast<size_t>(group) * a.d : nullptr;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float r[E];
+      Vec<T>::load(reinterpret_cast<const T*>(&raw[i]), r);
+      const int c0 = (i * 32 + lane) * E;
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        float4 k = gate ? __ldg(reinterpret_cast<const float4*>(gate + c0 + e)) : make_float4(1.f, 1.f, 1.f, 1.f);
+        if (a.scale) {
+          const float4 s = __ldg(reinterpret_cast<const float4*>(a.scale + c0 + e));
+          k.x *= s.x; k.y *= s.y; k.z *= s.z; k.w *= s.w;
+        }
+        v[i][e] = fmaf(k.x, v[i][e], r[e]);
+        v[i][e + 1] = fmaf(k.y, v[i][e + 1], r[e + 1]);
+        v[i][e + 2] = fmaf(k.z, v[i][e + 2], r[e + 2]);
+        v[i][e + 3] = fmaf(k.w, v[i][e + 3], r[e + 3]);
+      }
+      Vec<T>::store(x_out + row * a.d + c0, v[i]);
+    }
+    if (a.pre_g) {
+      norm_row<T, NV>(v, lane, a.d, a.pre_g, a.pre_b, a.eps, a.rms);
+      store_row<T, NV, Q8>(v, lane, xn, q8, qscale, row, a.d);
+    }
+  }
+}
+
+// any d (fp32 rows): one warp per row, scalar.  Only the lane that holds a column
+// reads or writes it, so x' may replace x and serves as the row's storage between
+// the two norms.
+__global__ void __launch_bounds__(256) norm_gate_generic_kernel(const float* x, const float* y, float* x_out, float* xn,
+                                                                const NormGateArgs a) {
+  const int lane = threadIdx.x & 31;
+  const size_t row = static_cast<size_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (row >= static_cast<size_t>(a.rows)) return;
+  const int group = norm_gate_group(a, row);
+  if (group < 0) return;
+  auto stats = [&](const float* v, float& mean, float& rstd) {
+    float s = 0.f, q = 0.f;
+    for (int c = lane; c < a.d; c += 32) s += v[c];
+    mean = a.rms ? 0.f : warp_sum(s) / a.d;
+    for (int c = lane; c < a.d; c += 32) {
+      const float t = v[c] - mean;
+      q = fmaf(t, t, q);
+    }
+    rstd = rsqrtf(warp_sum(q) / a.d + a.eps);
+  };
+  const size_t off = row * a.d;
+  const float* gate = a.gate ? a.gate + static_cast<size_t>(group) * a.d : nullptr;
+  float mean = 0.f, rstd = 1.f;
+  if (a.post_g) stats(y + off, mean, rstd);
+  for (int c = lane; c < a.d; c += 32) {
+    float v = y[off + c];
+    if (a.post_g) v = (v - mean) * rstd * a.post_g[c] + (a.rms ? 0.f : a.post_b[c]);
+    x_out[off + c] = fmaf((gate ? gate[c] : 1.f) * (a.scale ? a.scale[c] : 1.f), v, x[off + c]);
+  }
+  if (!a.pre_g) return;
+  stats(x_out + off, mean, rstd);
+  for (int c = lane; c < a.d; c += 32)
+    xn[off + c] = (x_out[off + c] - mean) * rstd * a.pre_g[c] + (a.rms ? 0.f : a.pre_b[c]);
+}
+
+// ---------------------------------------------------------------------------
 // Blend / merge ([TileShare] Fig. 2: overlap tokens' attention outputs blended with
 // w-bar; Fig. 3b: per-tile states merged).  Row u < U: fp32 sum over the token's
 // CSR entries in ascending tile order of wbar * P[ent]; row U + t*R + i: P[t*N + i].  One
 // warp writes each output row once; no atomics, so the result is deterministic.
 // ---------------------------------------------------------------------------
-template <typename T, int NV, bool Q8>
+template <typename T, int NV, int Q8>
 __global__ void __launch_bounds__(256) merge_kernel(const T* __restrict__ P, int rows, int U, int N, int R, int d,
                                                     const int* __restrict__ tok_ptr, const int* __restrict__ tok_ent,
                                                     const float* __restrict__ wbar, T* __restrict__ A,
@@ -206,7 +374,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const T* __restrict__ P, int
 // U + t*R + i is the single entry t*N + i with weight 1.  Sums run in ascending entry order,
 // as in merge_kernel.
 constexpr int kMergeWarps = 4;
-template <typename T, int NV, bool Q8>
+template <typename T, int NV, int Q8>
 __global__ void __launch_bounds__(kMergeWarps * 32) merge_bulk_kernel(
     const T* __restrict__ P, int rows, int U, int N, int R, int d, const int* __restrict__ tok_ptr,
     const int* __restrict__ tok_ent, const float* __restrict__ wbar, int cover, T* __restrict__ A,
@@ -449,6 +617,39 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const bf16* __restri
         *reinterpret_cast<uint2*>(q + row * cols + c0 + u * 256) = *reinterpret_cast<const uint2*>(pk);
       }
   }
+}
+
+// ---------------------------------------------------------------------------
+// Per-row quantisation of a bf16 matrix to signed 8-bit integers (row_quant_s8).
+// cols % 8 == 0.  One warp per row, the second pass reads the row again.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t bf16x8_abs_bits(const uint4& u) {   // largest magnitude of 8 bf16, as fp32 bits
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+  return m;
+}
+__device__ __forceinline__ uint2 bf16x8_to_s8(const uint4& u, const RowQuantS8& r) {
+  float f[8];
+  bf16x8_to_f32(u, f);
+  return make_uint2(quant_s8x4(f[0], f[1], f[2], f[3], r), quant_s8x4(f[4], f[5], f[6], f[7], r));
+}
+
+__global__ void __launch_bounds__(256) quantize_rows_s8_kernel(const bf16* __restrict__ x, int rows, int cols,
+                                                               uint8_t* __restrict__ q, float* __restrict__ scale) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const size_t row = static_cast<size_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (row >= static_cast<size_t>(rows)) return;
+  const bf16* xr = x + row * cols;
+  uint32_t amax = 0;
+  for (int c = lane * 8; c < cols; c += 256) amax = max(amax, bf16x8_abs_bits(*reinterpret_cast<const uint4*>(xr + c)));
+  const RowQuantS8 r = row_quant_s8(warp_max_u32(amax));
+  if (lane == 0) scale[row] = r.scale;
+  for (int c = lane * 8; c < cols; c += 256)
+    *reinterpret_cast<uint2*>(q + row * cols + c) = bf16x8_to_s8(*reinterpret_cast<const uint4*>(xr + c), r);
 }
 
 // ---------------------------------------------------------------------------

@@ -242,12 +242,14 @@ static cudaError_t launch_pdl_pair(void (*kern)(KArgs...), dim3 grid, dim3 block
 // model checks and RoPE tables
 // ============================================================================
 static int esize(ts_dtype dt) { return dt == TS_F32 ? 4 : 2; }
+// 8-bit GEMM operands with a scale per row of A and of W
+static bool has_q8(const ts_model_desc* m) { return m->dtype == TS_FP8_E4M3 || m->dtype == TS_INT8; }
 
 static ts_status check_model(const ts_model_desc* m) {
   if (!m) return fail(TS_ERR_INVALID_ARG, "model is NULL");
   if (m->d <= 0 || m->heads <= 0 || m->mlp <= 0 || m->d % m->heads)
     return fail(TS_ERR_INVALID_ARG, "bad model sizes d=%d heads=%d mlp=%d", m->d, m->heads, m->mlp);
-  if (m->dtype != TS_F32 && m->dtype != TS_BF16 && m->dtype != TS_FP8_E4M3)
+  if (m->dtype != TS_F32 && m->dtype != TS_BF16 && m->dtype != TS_FP8_E4M3 && m->dtype != TS_INT8)
     return fail(TS_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(m->dtype));
   const int hd = m->d / m->heads;
   int sum = 0;
@@ -305,10 +307,10 @@ static ts_status check_weights(const ts_model_desc* m, const ts_layer_weights* w
     if (!p) return fail(TS_ERR_INVALID_ARG, "a weight pointer is NULL");
     if (!aligned16(p)) return fail(TS_ERR_INVALID_ARG, "weight pointers must be 16-byte aligned");
   }
-  if (m->dtype == TS_FP8_E4M3) {
+  if (has_q8(m)) {
     const void* s[] = {w->s_qkv, w->s_o, w->s_1, w->s_2};
     for (const void* p : s)
-      if (!p || !aligned16(p)) return fail(TS_ERR_INVALID_ARG, "e4m3 weights need 16-byte aligned scales s_*");
+      if (!p || !aligned16(p)) return fail(TS_ERR_INVALID_ARG, "8-bit weights need 16-byte aligned scales s_*");
   }
   return TS_OK;
 }
@@ -322,7 +324,7 @@ struct Workspace {
   void* o;       // [T*N, d]  attention output
   void* a;       // [U+T, d]  blended attention output
   void* h;       // [Mx, f]   MLP hidden
-  uint8_t* q8;   // [Mx, max(d, f)] e4m3 GEMM operand
+  uint8_t* q8;   // [Mx, max(d, f)] 8-bit GEMM operand
   float* qs;     // [Mx]      its per-row scales
   void* X;       // [T*N, d]  per-tile state (stack)
   void* S;       // [U+T, d]  shared state (stack)
@@ -374,7 +376,7 @@ static Workspace layout(const ts_plan_s* p, const ts_model_desc* m, bool stack, 
   w.o = take(Mt * d * e);
   w.a = take(Ms * d * e);
   w.h = take(Mx * f * e);
-  if (m->dtype == TS_FP8_E4M3) {
+  if (has_q8(m)) {
     w.q8 = reinterpret_cast<uint8_t*>(take(Mx * std::max(d, f)));
     w.qs = reinterpret_cast<float*>(take(Mx * 4));
   }
@@ -404,7 +406,7 @@ static int num_sms() {
 
 static inline unsigned rows_grid(size_t rows) { return static_cast<unsigned>((rows + 7) / 8); }
 
-template <typename T, bool Q8>
+template <typename T, int Q8>
 static ts_status launch_layernorm_vec(const void* x, int rows, int d, const float* g, const float* b, float eps, int rms,
                                       void* y, uint8_t* q8, float* qs, const ts::RopeTable& rt, cudaStream_t st) {
   const unsigned fill_blocks = rt.cs ? static_cast<unsigned>((rt.total + 255) / 256) : 0u;
@@ -434,7 +436,7 @@ static ts_status launch_layernorm_vec(const void* x, int rows, int d, const floa
   return trace_post(st, "layernorm");
 }
 
-// y = Norm(x): LayerNorm, or RMSNorm for TS_BLOCK_RMS_SWIGLU (b unused); for e4m3
+// y = Norm(x): LayerNorm, or RMSNorm for TS_BLOCK_RMS_SWIGLU (b unused); with q8 set
 // writes q8/qs instead of y.
 static ts_status run_layernorm(const ts_model_desc* m, const void* x, int rows, const float* g, const float* b,
                                void* y, uint8_t* q8, float* qs, cudaStream_t st,
@@ -446,17 +448,78 @@ static ts_status run_layernorm(const ts_model_desc* m, const void* x, int rows, 
   set_work("layernorm", 0.0, static_cast<double>(rows) * d * (e + (q8 ? 1.0 : e)) + (q8 ? 4.0 * rows : 0.0));
   if (m->dtype == TS_F32) {
     if (d % 128 == 0 && d <= 1024)
-      return launch_layernorm_vec<float, false>(x, rows, d, g, b, m->eps_ln, rms, y, nullptr, nullptr, ts::RopeTable{}, st);
+      return launch_layernorm_vec<float, ts::ROW_T>(x, rows, d, g, b, m->eps_ln, rms, y, nullptr, nullptr, ts::RopeTable{}, st);
     trace_pre(st);
     ts::layernorm_generic_kernel<float><<<rows_grid(rows), 256, 0, st>>>(static_cast<const float*>(x), rows, d, g, b,
                                                                         m->eps_ln, rms, static_cast<float*>(y));
     return trace_post(st, "layernorm_generic");
   }
-  if (q8) return launch_layernorm_vec<bf16, true>(x, rows, d, g, b, m->eps_ln, rms, nullptr, q8, qs, rt, st);
-  return launch_layernorm_vec<bf16, false>(x, rows, d, g, b, m->eps_ln, rms, y, nullptr, nullptr, rt, st);
+  if (q8 && m->dtype == TS_INT8)
+    return launch_layernorm_vec<bf16, ts::ROW_S8>(x, rows, d, g, b, m->eps_ln, rms, nullptr, q8, qs, rt, st);
+  if (q8) return launch_layernorm_vec<bf16, ts::ROW_E4M3>(x, rows, d, g, b, m->eps_ln, rms, nullptr, q8, qs, rt, st);
+  return launch_layernorm_vec<bf16, ts::ROW_T>(x, rows, d, g, b, m->eps_ln, rms, y, nullptr, nullptr, rt, st);
 }
 
-template <typename T, bool Q8>
+template <typename T, int Q8>
+static ts_status launch_norm_gate_vec(const void* x, const void* y, void* x_out, void* xn, uint8_t* q8, float* qs,
+                                      const ts::NormGateArgs& a, cudaStream_t st) {
+  constexpr int E = ts::Vec<T>::E;
+  trace_pre(st);
+#define TS_NG_CASE(NV)                                                                                         \
+  case NV: {                                                                                                   \
+    auto kern = ts::norm_gate_kernel<T, NV, Q8>;                                                               \
+    static int occ = 0;                                                                                        \
+    if (occ <= 0) {                                                                                            \
+      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, 256, 0) != cudaSuccess || occ < 1) occ = 1; \
+    }                                                                                                          \
+    const unsigned grid = std::min<unsigned>(rows_grid(a.rows), static_cast<unsigned>(occ * num_sms()));       \
+    launch_pdl(kern, dim3(grid), dim3(256), 0, st, static_cast<const T*>(x), static_cast<const T*>(y),         \
+               static_cast<T*>(x_out), static_cast<T*>(xn), q8, qs, a);                                        \
+    break;                                                                                                     \
+  }
+  switch (a.d / (32 * E)) {
+    TS_NG_CASE(1) TS_NG_CASE(2) TS_NG_CASE(3) TS_NG_CASE(4) TS_NG_CASE(5) TS_NG_CASE(6) TS_NG_CASE(7) TS_NG_CASE(8)
+    default: return fail(TS_ERR_UNSUPPORTED, "norm_gate width %d", a.d);
+  }
+#undef TS_NG_CASE
+  return trace_post(st, "norm_gate");
+}
+
+// x_out = x + gate * scale * Norm_post(y); xn = Norm_pre(x_out) in the model dtype, or
+// q8/qs instead of xn where q8 is set (8-bit models).
+static ts_status run_norm_gate(const ts_model_desc* m, const ts_norm_gate* p, const void* x, const void* y,
+                               const int* row_group, int rows, void* x_out, void* xn, uint8_t* q8, float* qs,
+                               cudaStream_t st) {
+  if (rows == 0) return TS_OK;
+  ts::NormGateArgs a{};
+  a.rows = rows;
+  a.d = m->d;
+  a.groups = p->groups;
+  a.rms = m->block == TS_BLOCK_RMS_SWIGLU;
+  a.eps = m->eps_ln;
+  a.post_g = p->post_g;
+  a.post_b = p->post_b;
+  a.pre_g = p->pre_g;
+  a.pre_b = p->pre_b;
+  a.gate = p->gate;
+  a.scale = p->scale;
+  a.row_group = p->gate ? row_group : nullptr;
+  const double e = esize(m->dtype);
+  set_work("norm_gate", 0.0, static_cast<double>(rows) * m->d * (3.0 * e + (p->pre_g ? (q8 ? 1.0 : e) : 0.0)));
+  if (m->dtype == TS_F32) {
+    if (m->d % 128 == 0 && m->d <= 1024)
+      return launch_norm_gate_vec<float, ts::ROW_T>(x, y, x_out, xn, nullptr, nullptr, a, st);
+    trace_pre(st);
+    ts::norm_gate_generic_kernel<<<rows_grid(rows), 256, 0, st>>>(static_cast<const float*>(x), static_cast<const float*>(y),
+                                                                 static_cast<float*>(x_out), static_cast<float*>(xn), a);
+    return trace_post(st, "norm_gate_generic");
+  }
+  if (q8 && m->dtype == TS_INT8) return launch_norm_gate_vec<bf16, ts::ROW_S8>(x, y, x_out, nullptr, q8, qs, a, st);
+  if (q8) return launch_norm_gate_vec<bf16, ts::ROW_E4M3>(x, y, x_out, nullptr, q8, qs, a, st);
+  return launch_norm_gate_vec<bf16, ts::ROW_T>(x, y, x_out, xn, nullptr, nullptr, a, st);
+}
+
+template <typename T, int Q8>
 static ts_status launch_merge_vec(const ts_plan_s* p, const void* P, int rows, int d, void* A, uint8_t* q8,
                                   float* qs, cudaStream_t st) {
   constexpr int E = ts::Vec<T>::E;
@@ -521,23 +584,24 @@ static ts_status run_merge(const char* name, const ts_plan_s* p, const ts_model_
     set_work(name, 0.0, reads + writes);
   }
   if (m->dtype == TS_F32) {
-    if (d % 128 == 0 && d <= 1024) return launch_merge_vec<float, false>(p, P, rows, d, A, nullptr, nullptr, st);
+    if (d % 128 == 0 && d <= 1024) return launch_merge_vec<float, ts::ROW_T>(p, P, rows, d, A, nullptr, nullptr, st);
     trace_pre(st);
     ts::merge_generic_kernel<float><<<rows_grid(rows), 256, 0, st>>>(static_cast<const float*>(P), rows, p->U, p->N, p->R, d,
                                                                     p->d_tok_ptr, p->d_tok_ent, p->d_wbar,
                                                                     static_cast<float*>(A));
     return trace_post(st, "merge_generic");
   }
-  if (q8) return launch_merge_vec<bf16, true>(p, P, rows, d, nullptr, q8, qs, st);
-  return launch_merge_vec<bf16, false>(p, P, rows, d, A, nullptr, nullptr, st);
+  if (q8 && m->dtype == TS_INT8) return launch_merge_vec<bf16, ts::ROW_S8>(p, P, rows, d, nullptr, q8, qs, st);
+  if (q8) return launch_merge_vec<bf16, ts::ROW_E4M3>(p, P, rows, d, nullptr, q8, qs, st);
+  return launch_merge_vec<bf16, ts::ROW_T>(p, P, rows, d, A, nullptr, nullptr, st);
 }
 
-static ts_status run_quantize(const void* x, int rows, int cols, uint8_t* q, float* s, cudaStream_t st) {
+static ts_status run_quantize(ts_dtype dt, const void* x, int rows, int cols, uint8_t* q, float* s, cudaStream_t st) {
   if (rows == 0) return TS_OK;
-  set_work("quantize_e4m3", 0.0, static_cast<double>(rows) * cols * 3.0 + 4.0 * rows);
+  set_work(dt == TS_INT8 ? "quantize_i8" : "quantize_e4m3", 0.0, static_cast<double>(rows) * cols * 3.0 + 4.0 * rows);
   trace_pre(st);
-  launch_pdl(ts::quantize_rows_kernel, dim3(rows_grid(rows)), dim3(256), 0, st, static_cast<const bf16*>(x), rows, cols,
-             q, s);
+  auto kern = dt == TS_INT8 ? ts::quantize_rows_s8_kernel : ts::quantize_rows_kernel;
+  launch_pdl(kern, dim3(rows_grid(rows)), dim3(256), 0, st, static_cast<const bf16*>(x), rows, cols, q, s);
   return trace_post(st, "quantize_rows");
 }
 
@@ -546,11 +610,11 @@ static ts_status run_quantize(const void* x, int rows, int cols, uint8_t* q, flo
 // ---------------------------------------------------------------------------
 
 
-template <int BN, int STAGES, int EPI, bool FP8, int R0, int R1, int R2, int CG = 1>
+template <int BN, int STAGES, int EPI, int OPD, int R0, int R1, int R2, int CG = 1>
 static ts_status launch_gemm_tc(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& td,
                                 const ts::GemmArgs& args, cudaStream_t st) {
   using SM = ts::GemmSmem<BN, STAGES, CG>;
-  auto kern = ts::gemm_tc_kernel<BN, STAGES, EPI, FP8, R0, R1, R2, CG>;
+  auto kern = ts::gemm_tc_kernel<BN, STAGES, EPI, OPD, R0, R1, R2, CG>;
   static int configured[64] = {0};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -558,7 +622,7 @@ static ts_status launch_gemm_tc(const CUtensorMap& ta, const CUtensorMap& tb, co
     TS_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::LAUNCH_BYTES));
     configured[dev] = 1;
   }
-  const int tiles = ((args.M + 128 * CG - 1) / (128 * CG)) * (args.N / BN);
+  const int tiles = ((args.M + 128 * CG - 1) / (128 * CG)) * ((args.N + BN - 1) / BN);
   trace_pre(st);
   if (CG == 2) {
     // one pair per two SMs, both CTAs of a pair walking the same tiles
@@ -571,19 +635,19 @@ static ts_status launch_gemm_tc(const CUtensorMap& ta, const CUtensorMap& tb, co
   return trace_post(st, "gemm_tc");
 }
 
-template <int EPI, bool FP8, int R0, int R1, int R2>
+template <int EPI, int OPD, int R0, int R1, int R2>
 static ts_status dispatch_gemm_bn(int bn, bool pair, const CUtensorMap& ta, const CUtensorMap& tb,
                                   const CUtensorMap& td, const ts::GemmArgs& args, cudaStream_t st) {
   switch (bn) {
     case 256:
-      if (pair) return launch_gemm_tc<256, 6, EPI, FP8, R0, R1, R2, 2>(ta, tb, td, args, st);
-      return launch_gemm_tc<256, 4, EPI, FP8, R0, R1, R2>(ta, tb, td, args, st);
-    case 128: return launch_gemm_tc<128, 6, EPI, FP8, R0, R1, R2>(ta, tb, td, args, st);
+      if (pair) return launch_gemm_tc<256, 6, EPI, OPD, R0, R1, R2, 2>(ta, tb, td, args, st);
+      return launch_gemm_tc<256, 4, EPI, OPD, R0, R1, R2>(ta, tb, td, args, st);
+    case 128: return launch_gemm_tc<128, 6, EPI, OPD, R0, R1, R2>(ta, tb, td, args, st);
     default:
       if constexpr (EPI == ts::EPI_SWIGLU)   // SwiGLU tiles are at least 128 wide
-        return launch_gemm_tc<128, 6, EPI, FP8, R0, R1, R2>(ta, tb, td, args, st);
+        return launch_gemm_tc<128, 6, EPI, OPD, R0, R1, R2>(ta, tb, td, args, st);
       else
-        return launch_gemm_tc<64, 8, EPI, FP8, R0, R1, R2>(ta, tb, td, args, st);
+        return launch_gemm_tc<64, 8, EPI, OPD, R0, R1, R2>(ta, tb, td, args, st);
   }
 }
 
@@ -601,21 +665,22 @@ static bool gemm_pairs_enabled() {
 // Output tile width for the persistent GEMM: the persistent CTAs walk the tiles
 // round-robin, so the busiest CTA handles ceil(tiles / SMs) tiles.  Cost model:
 // that count times (BN + 48), 48 columns standing for the fixed per-tile work
-// (pipeline fill, epilogue tail); ties go to the wider tile.
-static int pick_bn(int M, int N) {
+// (pipeline fill, epilogue tail); ties go to the wider tile.  ragged: the last
+// column tile may end past N (integer products).
+static int pick_bn(int M, int N, bool ragged = false) {
   // tuning override: TS_GEMM_BN=64|128|256 forces the tile width where it divides N
   static const int forced = [] {
     const char* e = std::getenv("TS_GEMM_BN");
     return e ? std::atoi(e) : 0;
   }();
-  if ((forced == 64 || forced == 128 || forced == 256) && N % forced == 0) return forced;
+  if ((forced == 64 || forced == 128 || forced == 256) && (ragged || N % forced == 0)) return forced;
   const int mt = (M + 127) / 128;
   const int sms = num_sms();
   int best = 64;
   long best_cost = -1;
   for (int bn : {256, 128, 64}) {
-    if (N % bn) continue;
-    const long tiles = static_cast<long>(mt) * (N / bn);
+    if (N % bn && !ragged) continue;
+    const long tiles = static_cast<long>(mt) * ((N + bn - 1) / bn);
     const long cost = ((tiles + sms - 1) / sms) * (bn + 48);
     if (best_cost < 0 || cost < best_cost) {
       best = bn;
@@ -625,30 +690,43 @@ static int pick_bn(int M, int N) {
   return best;
 }
 
-// Y[M, N] = A[M, K] W[N, K]^T with epilogue; A bf16 (or e4m3 + a_scale), W bf16 (or e4m3 + w_scale).
+// Sizes the tensor-core GEMMs take.  Integer sums stay exact in int32: at most
+// K * 128 * 128 < 2^31.
+static constexpr int kInt8MaxK = 131056;
+static ts_status check_gemm_sizes(const ts_model_desc* m, int K, int N) {
+  if (m->dtype == TS_INT8) {
+    if (K % 16 || N % 8) return fail(TS_ERR_UNSUPPORTED, "int8 GEMM needs K %% 16 == 0 and N %% 8 == 0 (K=%d N=%d)", K, N);
+    if (K > kInt8MaxK) return fail(TS_ERR_UNSUPPORTED, "int8 GEMM takes K <= %d (K=%d): larger sums could leave int32", kInt8MaxK, K);
+    return TS_OK;
+  }
+  if (K % (m->dtype == TS_FP8_E4M3 ? 128 : 64) || N % 64) return fail(TS_ERR_UNSUPPORTED, "GEMM sizes K=%d N=%d not tiled", K, N);
+  return TS_OK;
+}
+
+// Y[M, N] = A[M, K] W[N, K]^T with epilogue; A bf16 (or 8-bit + a_scale), W bf16 (or 8-bit + w_scale).
 // EPI_SWIGLU: N is the output width and W, bias, w_scale have 2N rows (gate, then up).
 static ts_status run_gemm_tc(const char* name, const ts_model_desc* m, int epi, const void* A, const float* a_scale,
                              const void* W, const float* w_scale, int M, int N, int K, const float* bias, bf16* out,
                              const ts_layer_weights* qk, const int* pos, cudaStream_t st,
                              const ts::RopeTable& rt = ts::RopeTable{}) {
   if (M == 0) return TS_OK;
-  const bool fp8 = m->dtype == TS_FP8_E4M3;
+  const bool q8 = has_q8(m), s8 = m->dtype == TS_INT8;
   const bool glu = epi == ts::EPI_SWIGLU;
   const int NA = glu ? 2 * N : N;   // accumulator columns = rows of W
   {
-    const double ea = fp8 ? 1.0 : 2.0;
+    const double ea = q8 ? 1.0 : 2.0;
     const double bytes = static_cast<double>(M) * K * ea + static_cast<double>(NA) * K * ea +
                          static_cast<double>(M) * N * 2.0 * (epi == ts::EPI_RESID ? 2.0 : 1.0);
     set_work(name, 2.0 * M * static_cast<double>(NA) * K, bytes);
   }
-  if (K % (fp8 ? 128 : 64) || N % 64) return fail(TS_ERR_UNSUPPORTED, "GEMM sizes K=%d N=%d not tiled", K, N);
-  int bn = pick_bn(M, NA);
-  if (glu && bn < 128) bn = 128;    // NA = 2N is a multiple of 128
+  TS_TRY(check_gemm_sizes(m, K, N));
+  int bn = pick_bn(M, NA, s8);
+  if (glu && bn < 128) bn = 128;    // NA = 2N is a multiple of 128, or the last tile is clipped (int8)
   // 256-wide tiles of tall GEMMs run as two-SM pairs of 256 x 256 tiles
   const bool pair = bn == 256 && M >= kGemmPairMinRows && gemm_pairs_enabled();
   CUtensorMap ta, tb, td;
-  TS_TRY(make_tmap(&ta, A, M, K, fp8 ? 1 : 2, 128));
-  TS_TRY(make_tmap(&tb, W, NA, K, fp8 ? 1 : 2, (glu || pair) ? bn / 2 : bn));
+  TS_TRY(make_tmap(&ta, A, M, K, q8 ? 1 : 2, 128));
+  TS_TRY(make_tmap(&tb, W, NA, K, q8 ? 1 : 2, (glu || pair) ? bn / 2 : bn));
   TS_TRY(make_tmap(&td, out, M, N, 2, 32));   // output (and residual): 32 x 64 chunks of the epilogue warps
   ts::GemmArgs g{};
   g.M = M;
@@ -670,8 +748,9 @@ static ts_status run_gemm_tc(const char* name, const ts_model_desc* m, int epi, 
   }
   const bool r3 = m->rope_dims[0] == 16;
 #define TS_GEMM_EPI(E, R0, R1, R2) \
-  (fp8 ? dispatch_gemm_bn<E, true, R0, R1, R2>(bn, pair, ta, tb, td, g, st)     \
-       : dispatch_gemm_bn<E, false, R0, R1, R2>(bn, pair, ta, tb, td, g, st))
+  (s8   ? dispatch_gemm_bn<E, ts::OPD_S8, R0, R1, R2>(bn, pair, ta, tb, td, g, st)     \
+   : q8 ? dispatch_gemm_bn<E, ts::OPD_E4M3, R0, R1, R2>(bn, pair, ta, tb, td, g, st)   \
+        : dispatch_gemm_bn<E, ts::OPD_BF16, R0, R1, R2>(bn, pair, ta, tb, td, g, st))
   switch (epi) {
     case ts::EPI_BIAS: return TS_GEMM_EPI(ts::EPI_BIAS, 0, 32, 32);
     case ts::EPI_GELU: return TS_GEMM_EPI(ts::EPI_GELU, 0, 32, 32);
@@ -798,7 +877,7 @@ static ts_status run_qkv(const ts_plan_s* p, const ts_model_desc* m, const ts_la
   }
   // LN1 also fills the RoPE table that the QKV epilogue reads
   const ts::RopeTable rt = make_rope_table(p, m, ws.rope);
-  if (m->dtype == TS_FP8_E4M3) {
+  if (has_q8(m)) {
     TS_TRY(run_layernorm(m, state, rows, w->ln1_g, w->ln1_b, nullptr, ws.q8, ws.qs, st, rt));
     return run_gemm_tc("gemm_qkv", m, ts::EPI_QKV, ws.q8, ws.qs, w->w_qkv, w->s_qkv, rows, 3 * d, d, w->b_qkv,
                        static_cast<bf16*>(qkv), w, pos, st, rt);
@@ -815,12 +894,38 @@ static ts_status run_out_proj(const ts_model_desc* m, const ts_layer_weights* w,
   if (m->dtype == TS_F32)
     return run_gemm_f32("gemm_out", ts::EPI_RESID, static_cast<const float*>(att), static_cast<const float*>(w->w_o), rows, d, d,
                         w->b_o, static_cast<float*>(state), st);
-  if (m->dtype == TS_FP8_E4M3) {
-    if (!att_quantised) TS_TRY(run_quantize(att, rows, d, ws.q8, ws.qs, st));
+  if (has_q8(m)) {
+    if (!att_quantised) TS_TRY(run_quantize(m->dtype, att, rows, d, ws.q8, ws.qs, st));
     return run_gemm_tc("gemm_out", m, ts::EPI_RESID, ws.q8, ws.qs, w->w_o, w->s_o, rows, d, d, w->b_o, static_cast<bf16*>(state),
                        nullptr, nullptr, st);
   }
   return run_gemm_tc("gemm_out", m, ts::EPI_RESID, att, nullptr, w->w_o, nullptr, rows, d, d, w->b_o, static_cast<bf16*>(state),
+                     nullptr, nullptr, st);
+}
+
+// out (+)= W2 act(W1 xn + b1) + b2 of rows that Norm2 has written (ws.xn, or ws.q8 and
+// ws.qs for 8-bit models); resid: out is the residual stream, else out is written.
+static ts_status run_mlp_normed(const ts_model_desc* m, const ts_layer_weights* w, int rows, void* out, bool resid,
+                                const Workspace& ws, cudaStream_t st) {
+  const int d = m->d, f = m->mlp;
+  const int up = m->block == TS_BLOCK_RMS_SWIGLU ? ts::EPI_SWIGLU : ts::EPI_GELU;
+  const int down = resid ? ts::EPI_RESID : ts::EPI_BIAS;
+  if (m->dtype == TS_F32) {
+    TS_TRY(run_gemm_f32("gemm_up", up, static_cast<const float*>(ws.xn), static_cast<const float*>(w->w_1), rows, f, d,
+                        w->b_1, static_cast<float*>(ws.h), st));
+    return run_gemm_f32("gemm_down", down, static_cast<const float*>(ws.h), static_cast<const float*>(w->w_2), rows, d, f,
+                        w->b_2, static_cast<float*>(out), st);
+  }
+  if (has_q8(m)) {
+    TS_TRY(run_gemm_tc("gemm_up", m, up, ws.q8, ws.qs, w->w_1, w->s_1, rows, f, d, w->b_1, static_cast<bf16*>(ws.h),
+                       nullptr, nullptr, st));
+    TS_TRY(run_quantize(m->dtype, ws.h, rows, f, ws.q8, ws.qs, st));
+    return run_gemm_tc("gemm_down", m, down, ws.q8, ws.qs, w->w_2, w->s_2, rows, d, f, w->b_2, static_cast<bf16*>(out),
+                       nullptr, nullptr, st);
+  }
+  TS_TRY(run_gemm_tc("gemm_up", m, up, ws.xn, nullptr, w->w_1, nullptr, rows, f, d, w->b_1, static_cast<bf16*>(ws.h),
+                     nullptr, nullptr, st));
+  return run_gemm_tc("gemm_down", m, down, ws.h, nullptr, w->w_2, nullptr, rows, d, f, w->b_2, static_cast<bf16*>(out),
                      nullptr, nullptr, st);
 }
 
@@ -829,29 +934,9 @@ static ts_status run_out_proj(const ts_model_desc* m, const ts_layer_weights* w,
 // when out == in), else out is written.
 static ts_status run_mlp_any(const ts_model_desc* m, const ts_layer_weights* w, int rows, const void* in, void* out,
                              bool resid, const Workspace& ws, cudaStream_t st) {
-  const int d = m->d, f = m->mlp;
-  const int up = m->block == TS_BLOCK_RMS_SWIGLU ? ts::EPI_SWIGLU : ts::EPI_GELU;
-  const int down = resid ? ts::EPI_RESID : ts::EPI_BIAS;
-  if (m->dtype == TS_F32) {
-    TS_TRY(run_layernorm(m, in, rows, w->ln2_g, w->ln2_b, ws.xn, nullptr, nullptr, st));
-    TS_TRY(run_gemm_f32("gemm_up", up, static_cast<const float*>(ws.xn), static_cast<const float*>(w->w_1), rows, f, d,
-                        w->b_1, static_cast<float*>(ws.h), st));
-    return run_gemm_f32("gemm_down", down, static_cast<const float*>(ws.h), static_cast<const float*>(w->w_2), rows, d, f,
-                        w->b_2, static_cast<float*>(out), st);
-  }
-  if (m->dtype == TS_FP8_E4M3) {
-    TS_TRY(run_layernorm(m, in, rows, w->ln2_g, w->ln2_b, nullptr, ws.q8, ws.qs, st));
-    TS_TRY(run_gemm_tc("gemm_up", m, up, ws.q8, ws.qs, w->w_1, w->s_1, rows, f, d, w->b_1, static_cast<bf16*>(ws.h),
-                       nullptr, nullptr, st));
-    TS_TRY(run_quantize(ws.h, rows, f, ws.q8, ws.qs, st));
-    return run_gemm_tc("gemm_down", m, down, ws.q8, ws.qs, w->w_2, w->s_2, rows, d, f, w->b_2, static_cast<bf16*>(out),
-                       nullptr, nullptr, st);
-  }
-  TS_TRY(run_layernorm(m, in, rows, w->ln2_g, w->ln2_b, ws.xn, nullptr, nullptr, st));
-  TS_TRY(run_gemm_tc("gemm_up", m, up, ws.xn, nullptr, w->w_1, nullptr, rows, f, d, w->b_1, static_cast<bf16*>(ws.h),
-                     nullptr, nullptr, st));
-  return run_gemm_tc("gemm_down", m, down, ws.h, nullptr, w->w_2, nullptr, rows, d, f, w->b_2, static_cast<bf16*>(out),
-                     nullptr, nullptr, st);
+  const bool q = has_q8(m);
+  TS_TRY(run_layernorm(m, in, rows, w->ln2_g, w->ln2_b, q ? nullptr : ws.xn, q ? ws.q8 : nullptr, q ? ws.qs : nullptr, st));
+  return run_mlp_normed(m, w, rows, out, resid, ws, st);
 }
 
 // state += MLP(state)
@@ -896,8 +981,8 @@ static ts_status run_out_bias(const ts_model_desc* m, const ts_layer_weights* w,
   if (m->dtype == TS_F32)
     return run_gemm_f32("gemm_out", ts::EPI_BIAS, static_cast<const float*>(att), static_cast<const float*>(w->w_o), rows, d, d,
                         w->b_o, static_cast<float*>(out), st);
-  if (m->dtype == TS_FP8_E4M3) {
-    if (!att_quantised) TS_TRY(run_quantize(att, rows, d, ws.q8, ws.qs, st));
+  if (has_q8(m)) {
+    if (!att_quantised) TS_TRY(run_quantize(m->dtype, att, rows, d, ws.q8, ws.qs, st));
     return run_gemm_tc("gemm_out", m, ts::EPI_BIAS, ws.q8, ws.qs, w->w_o, w->s_o, rows, d, d, w->b_o, static_cast<bf16*>(out),
                        nullptr, nullptr, st);
   }
@@ -928,10 +1013,44 @@ static ts_status layer_shared(const ts_plan_s* p, const ts_model_desc* m, const 
   const int rows = p->U + p->G;
   TS_TRY(run_qkv(p, m, w, true, S, ws.qkv, ws, st));
   TS_TRY(run_attention(p, m, true, ws.qkv, ws.o, st));
-  const bool q = m->dtype == TS_FP8_E4M3;
+  const bool q = has_q8(m);
   TS_TRY(run_merge("blend", p, m, ws.o, rows, q ? nullptr : ws.a, q ? ws.q8 : nullptr, q ? ws.qs : nullptr, st));
   TS_TRY(run_out_proj(m, w, ws.a, q, rows, S, ws, st));
   return run_mlp(m, w, rows, S, ws, st);
+}
+
+// Sandwich layer (shared or per tile): each half's output passes a norm, a gate and a
+// residual scale on its way into the residual stream, in the pass that also writes
+// Norm2 of the stream for the MLP (8-bit models: already quantised).  The halves'
+// outputs live in the q/k/v region, which the attention has finished with.
+static ts_status layer_sandwich(const ts_plan_s* p, const ts_model_desc* m, const ts_layer_weights* w,
+                                const ts_sandwich_weights* sw, bool shared, void* state, const Workspace& ws,
+                                cudaStream_t st) {
+  const int rows = shared ? p->U + p->G : p->T * p->N;
+  const bool q = has_q8(m);
+  TS_TRY(run_qkv(p, m, w, shared, state, ws.qkv, ws, st));
+  TS_TRY(run_attention(p, m, shared, ws.qkv, ws.o, st));
+  if (shared)
+    TS_TRY(run_merge("blend", p, m, ws.o, rows, q ? nullptr : ws.a, q ? ws.q8 : nullptr, q ? ws.qs : nullptr, st));
+  void* branch = ws.qkv;
+  TS_TRY(run_out_bias(m, w, shared ? ws.a : ws.o, shared && q, rows, branch, ws, st));
+  ts_norm_gate ng{};
+  ng.post_g = sw->post1_g;
+  ng.post_b = sw->post1_b;
+  ng.pre_g = w->ln2_g;
+  ng.pre_b = w->ln2_b;
+  ng.gate = sw->gate1;
+  ng.scale = sw->scale1;
+  ng.groups = sw->groups;
+  TS_TRY(run_norm_gate(m, &ng, state, branch, sw->row_group, rows, state, q ? nullptr : ws.xn, q ? ws.q8 : nullptr, q ? ws.qs : nullptr, st));
+  TS_TRY(run_mlp_normed(m, w, rows, branch, false, ws, st));
+  ng.post_g = sw->post2_g;
+  ng.post_b = sw->post2_b;
+  ng.pre_g = nullptr;
+  ng.pre_b = nullptr;
+  ng.gate = sw->gate2;
+  ng.scale = sw->scale2;
+  return run_norm_gate(m, &ng, state, branch, sw->row_group, rows, state, nullptr, nullptr, nullptr, st);
 }
 
 // Partial sharing ([TileShare] Tab. 1 top): per-tile residual streams X, the
@@ -940,7 +1059,7 @@ static ts_status layer_shared(const ts_plan_s* p, const ts_model_desc* m, const 
 static ts_status layer_partial(const ts_plan_s* p, const ts_model_desc* m, const ts_layer_weights* w, unsigned ops,
                                void* X, const Workspace& ws, cudaStream_t st) {
   const int rows_t = p->T * p->N, rows_s = p->U + p->G;
-  const bool q8 = m->dtype == TS_FP8_E4M3;
+  const bool q8 = has_q8(m);
   if (ops & TS_SHARE_QKV) {
     TS_TRY(run_merge("merge", p, m, X, rows_s, ws.sm, nullptr, nullptr, st));
     TS_TRY(run_qkv(p, m, w, true, ws.sm, ws.qkv, ws, st));
@@ -972,6 +1091,51 @@ static ts_status check_ws(const ts_plan_s* p, const ts_model_desc* m, bool stack
   if (ws_bytes < need.bytes) return fail(TS_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need.bytes);
   *out = layout(p, m, stack, static_cast<char*>(ws));
   return TS_OK;
+}
+
+// norms, gate and scale of one half: vectors aligned, biases where LayerNorm needs them
+static ts_status check_norm_gate(const ts_model_desc* m, const ts_norm_gate* p) {
+  if (!p) return fail(TS_ERR_INVALID_ARG, "the norm and gate descriptor is NULL");
+  const bool rms = m->block == TS_BLOCK_RMS_SWIGLU;
+  if (!rms && ((p->post_g && !p->post_b) || (p->pre_g && !p->pre_b)))
+    return fail(TS_ERR_INVALID_ARG, "LayerNorm needs a bias beside its gain");
+  const void* v[] = {p->post_g, p->post_b, p->pre_g, p->pre_b, p->gate, p->scale};
+  for (const void* q : v)
+    if (q && !aligned16(q)) return fail(TS_ERR_INVALID_ARG, "norm, gate and scale vectors must be 16-byte aligned");
+  if (p->gate && p->groups < 1) return fail(TS_ERR_INVALID_ARG, "a gate needs groups >= 1");
+  return TS_OK;
+}
+
+static ts_status check_row_group(const int* g) {
+  if (reinterpret_cast<uintptr_t>(g) & 3u) return fail(TS_ERR_INVALID_ARG, "row_group must be 4-byte aligned");
+  return TS_OK;
+}
+
+static ts_status check_sandwich(const ts_model_desc* m, const ts_sandwich_weights* sw) {
+  if (!sw) return fail(TS_ERR_INVALID_ARG, "sandwich weights are NULL");
+  for (int i = 0; i < 2; ++i) {
+    ts_norm_gate ng{};
+    ng.post_g = i ? sw->post2_g : sw->post1_g;
+    ng.post_b = i ? sw->post2_b : sw->post1_b;
+    ng.gate = i ? sw->gate2 : sw->gate1;
+    ng.scale = i ? sw->scale2 : sw->scale1;
+    ng.groups = sw->groups;
+    TS_TRY(check_norm_gate(m, &ng));
+  }
+  return check_row_group(sw->row_group);
+}
+
+static ts_status block_sandwich(ts_plan_t p, const ts_model_desc* m, const ts_layer_weights* w,
+                                const ts_sandwich_weights* sw, bool shared, void* state, void* ws, size_t ws_bytes,
+                                void* stream) {
+  TS_TRY(check_plan(p));
+  TS_TRY(check_model(m));
+  TS_TRY(check_weights(m, w));
+  TS_TRY(check_sandwich(m, sw));
+  if (!state || !aligned16(state)) return fail(TS_ERR_INVALID_ARG, "the state must be a 16-byte aligned device pointer");
+  Workspace W;
+  TS_TRY(check_ws(p, m, false, ws, ws_bytes, &W));
+  return layer_sandwich(p, m, w, sw, shared, state, W, static_cast<cudaStream_t>(stream));
 }
 
 // ============================================================================
@@ -1211,6 +1375,16 @@ ts_status ts_block_partial(ts_plan_t p, const ts_model_desc* m, const ts_layer_w
   return layer_partial(p, m, w, shared_ops, X, W, static_cast<cudaStream_t>(stream));
 }
 
+ts_status ts_block_shared_sandwich(ts_plan_t p, const ts_model_desc* m, const ts_layer_weights* w,
+                                   const ts_sandwich_weights* sw, void* S, void* ws, size_t ws_bytes, void* stream) {
+  return block_sandwich(p, m, w, sw, true, S, ws, ws_bytes, stream);
+}
+
+ts_status ts_block_tiled_sandwich(ts_plan_t p, const ts_model_desc* m, const ts_layer_weights* w,
+                                  const ts_sandwich_weights* sw, void* X, void* ws, size_t ws_bytes, void* stream) {
+  return block_sandwich(p, m, w, sw, false, X, ws, ws_bytes, stream);
+}
+
 // ---------------------------------------------------------------------------
 // Shared layer with its scratch in a static device array (no allocation).
 // ---------------------------------------------------------------------------
@@ -1296,9 +1470,9 @@ ts_status ts_block_shared_noalloc(ts_plan_t p, const ts_model_desc* m, const ts_
   void* base = nullptr;
   TS_TRY(noalloc_scratch(&base));
   const Workspace W = layout(p, m, false, static_cast<char*>(base), true);
-  // layer_shared reads the regions xn, qkv, o, a, h, rope (and q8, qs for e4m3)
+  // layer_shared reads the regions xn, qkv, o, a, h, rope (and q8, qs for 8-bit models)
   // and no others (not X, S or sm, which the shared-only layout leaves null)
-  if (!W.xn || !W.qkv || !W.o || !W.a || !W.h || !W.rope || (m->dtype == TS_FP8_E4M3 && (!W.q8 || !W.qs)))
+  if (!W.xn || !W.qkv || !W.o || !W.a || !W.h || !W.rope || (has_q8(m) && (!W.q8 || !W.qs)))
     return fail(TS_ERR_WORKSPACE, "ts_block_shared_noalloc: scratch layout incomplete");
   return layer_shared(p, m, w, S, W, static_cast<cudaStream_t>(stream));
 }
@@ -1334,7 +1508,14 @@ ts_status ts_quantize_rows_e4m3(const void* x, int rows, int cols, void* q, floa
   if (!x || !q || !scale) return fail(TS_ERR_INVALID_ARG, "NULL argument");
   if (rows < 0 || cols <= 0 || cols % 8) return fail(TS_ERR_INVALID_ARG, "need rows >= 0, cols %% 8 == 0");
   if (!aligned16(x) || !aligned16(q) || !aligned16(scale)) return fail(TS_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
-  return run_quantize(x, rows, cols, static_cast<uint8_t*>(q), scale, static_cast<cudaStream_t>(stream));
+  return run_quantize(TS_FP8_E4M3, x, rows, cols, static_cast<uint8_t*>(q), scale, static_cast<cudaStream_t>(stream));
+}
+
+ts_status ts_quantize_rows_i8(const void* x, int rows, int cols, void* q, float* scale, void* stream) {
+  if (!x || !q || !scale) return fail(TS_ERR_INVALID_ARG, "NULL argument");
+  if (rows < 0 || cols <= 0 || cols % 8) return fail(TS_ERR_INVALID_ARG, "need rows >= 0, cols %% 8 == 0");
+  if (!aligned16(x) || !aligned16(q) || !aligned16(scale)) return fail(TS_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+  return run_quantize(TS_INT8, x, rows, cols, static_cast<uint8_t*>(q), scale, static_cast<cudaStream_t>(stream));
 }
 
 ts_status ts_device_status(void) {
@@ -1368,29 +1549,67 @@ ts_status ts_op_layernorm(const ts_model_desc* m, const void* x, int rows, const
   return run_layernorm(m, x, rows, g, b, y, nullptr, nullptr, static_cast<cudaStream_t>(stream));
 }
 
+ts_status ts_op_norm_gate(const ts_model_desc* m, const ts_norm_gate* p, const void* x, const void* y,
+                          const int* row_group, int rows, void* x_out, void* xn, float* xn_scale, void* stream) {
+  TS_TRY(check_model(m));
+  TS_TRY(check_norm_gate(m, p));
+  TS_TRY(check_row_group(row_group));
+  if (!x || !y || !x_out || rows < 0) return fail(TS_ERR_INVALID_ARG, "bad argument");
+  if ((p->pre_g != nullptr) != (xn != nullptr)) return fail(TS_ERR_INVALID_ARG, "xn goes with pre_g: both or neither");
+  if (xn_scale && !xn) return fail(TS_ERR_INVALID_ARG, "xn_scale needs xn");
+  if (xn_scale && !has_q8(m)) return fail(TS_ERR_INVALID_ARG, "xn_scale needs an 8-bit model (TS_FP8_E4M3 or TS_INT8)");
+  if (!aligned16(x) || !aligned16(y) || !aligned16(x_out) || !aligned16(xn) || !aligned16(xn_scale))
+    return fail(TS_ERR_INVALID_ARG, "alignment");
+  return run_norm_gate(m, p, x, y, row_group, rows, x_out, xn_scale ? nullptr : xn, xn_scale ? static_cast<uint8_t*>(xn) : nullptr,
+                       xn_scale, static_cast<cudaStream_t>(stream));
+}
+
+static ts_status epilogue_of(ts_epilogue epi, int* e) {
+  switch (epi) {
+    case TS_EPI_BIAS: *e = ts::EPI_BIAS; return TS_OK;
+    case TS_EPI_BIAS_GELU: *e = ts::EPI_GELU; return TS_OK;
+    case TS_EPI_BIAS_RESID: *e = ts::EPI_RESID; return TS_OK;
+    case TS_EPI_BIAS_SWIGLU: *e = ts::EPI_SWIGLU; return TS_OK;
+  }
+  return fail(TS_ERR_INVALID_ARG, "unknown epilogue");
+}
+
 ts_status ts_op_linear(const ts_model_desc* m, const void* x, int rows, int K, const void* W, const float* w_scale,
                        int N, const float* bias, ts_epilogue epi, void* y, void* scratch, void* stream) {
   TS_TRY(check_model(m));
   if (!x || !W || !y || !bias || rows < 0 || K <= 0 || N <= 0) return fail(TS_ERR_INVALID_ARG, "bad argument");
   if (!aligned16(x) || !aligned16(W) || !aligned16(y) || !aligned16(bias)) return fail(TS_ERR_INVALID_ARG, "alignment");
-  if (epi != TS_EPI_BIAS && epi != TS_EPI_BIAS_GELU && epi != TS_EPI_BIAS_RESID && epi != TS_EPI_BIAS_SWIGLU)
-    return fail(TS_ERR_INVALID_ARG, "unknown epilogue");
-  const int e = epi == TS_EPI_BIAS        ? ts::EPI_BIAS
-                : epi == TS_EPI_BIAS_GELU ? ts::EPI_GELU
-                : epi == TS_EPI_BIAS_RESID ? ts::EPI_RESID
-                                           : ts::EPI_SWIGLU;
+  int e = 0;
+  TS_TRY(epilogue_of(epi, &e));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (m->dtype == TS_F32)
     return run_gemm_f32("linear", e, static_cast<const float*>(x), static_cast<const float*>(W), rows, N, K, bias,
                         static_cast<float*>(y), st);
-  if (m->dtype == TS_FP8_E4M3) {
-    if (!scratch || !aligned16(scratch) || !w_scale) return fail(TS_ERR_INVALID_ARG, "e4m3 linear needs scratch and w_scale");
+  TS_TRY(check_gemm_sizes(m, K, N));
+  if (has_q8(m)) {
+    if (!scratch || !aligned16(scratch) || !w_scale || !aligned16(w_scale))
+      return fail(TS_ERR_INVALID_ARG, "8-bit linear needs scratch and w_scale, 16-byte aligned");
     uint8_t* q8 = static_cast<uint8_t*>(scratch);
-    float* qs = reinterpret_cast<float*>(q8 + align256(static_cast<size_t>(rows) * K));
-    TS_TRY(run_quantize(x, rows, K, q8, qs, st));
+    float* qs = reinterpret_cast<float*>(q8 + static_cast<size_t>(rows) * K);   // K % 16 == 0 keeps it aligned
+    TS_TRY(run_quantize(m->dtype, x, rows, K, q8, qs, st));
     return run_gemm_tc("linear", m, e, q8, qs, W, w_scale, rows, N, K, bias, static_cast<bf16*>(y), nullptr, nullptr, st);
   }
   return run_gemm_tc("linear", m, e, x, nullptr, W, nullptr, rows, N, K, bias, static_cast<bf16*>(y), nullptr, nullptr, st);
+}
+
+ts_status ts_op_linear_q8(const ts_model_desc* m, const void* x, const float* x_scale, int rows, int K, const void* W,
+                          const float* w_scale, int N, const float* bias, ts_epilogue epi, void* y, void* stream) {
+  TS_TRY(check_model(m));
+  if (!has_q8(m)) return fail(TS_ERR_INVALID_ARG, "ts_op_linear_q8 needs an 8-bit model (TS_FP8_E4M3 or TS_INT8)");
+  if (!x || !x_scale || !W || !w_scale || !y || !bias || rows < 0 || K <= 0 || N <= 0)
+    return fail(TS_ERR_INVALID_ARG, "bad argument");
+  if (!aligned16(x) || !aligned16(x_scale) || !aligned16(W) || !aligned16(w_scale) || !aligned16(y) || !aligned16(bias))
+    return fail(TS_ERR_INVALID_ARG, "alignment");
+  int e = 0;
+  TS_TRY(epilogue_of(epi, &e));
+  TS_TRY(check_gemm_sizes(m, K, N));
+  return run_gemm_tc("linear", m, e, x, x_scale, W, w_scale, rows, N, K, bias, static_cast<bf16*>(y), nullptr, nullptr,
+                     static_cast<cudaStream_t>(stream));
 }
 
 ts_status ts_op_qkv(ts_plan_t p, const ts_model_desc* m, const ts_layer_weights* w, ts_rows_mode mode,

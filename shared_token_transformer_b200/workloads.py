@@ -30,7 +30,7 @@ class Config:
     d: int
     heads: int
     mlp: int
-    dtype: str            # "f32", "bf16" or "fp8" (e4m3 GEMMs, bf16 activations)
+    dtype: str            # "f32", "bf16", "fp8" or "int8" (8-bit GEMMs, bf16 activations)
     L: int
     k: int
     rope_dims: tuple      # channels of the head dimension given to the (f, y, x) axes
@@ -105,7 +105,7 @@ def round_to(a: np.ndarray, dtype: str) -> np.ndarray:
     t = torch.from_numpy(np.ascontiguousarray(a, dtype=np.float64))
     if dtype == "f32":
         return t.to(torch.float32).to(torch.float64).numpy()
-    if dtype in ("bf16", "fp8"):
+    if dtype in ("bf16", "fp8", "int8"):
         return t.to(torch.bfloat16).to(torch.float64).numpy()
     raise ValueError(dtype)
 
