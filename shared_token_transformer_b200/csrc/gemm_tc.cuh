@@ -12,10 +12,8 @@
 //              W holds N/2 gate rows above N/2 up rows; a 128 x BN tile loads BN/2
 //              gate rows and the BN/2 matching up rows, so the two sums of an
 //              output sit in one accumulator, BN/2 columns apart; y is [M, N/2].
-// For 8-bit operands (e4m3, or signed integers with exact int32 sums) acc is first
-// multiplied by the row scale of A and the column scale of W.  Integer products take
-// any K % 16 == 0 and N % 8 == 0: the copies fill K past the end with zeros and clip
-// columns past N.
+// For e4m3 operands acc is first multiplied by the row scale of A and the column
+// scale of W.
 //
 // Kernel design: persistent, warp-specialised, 320 threads, CTAs walk the
 // 128 x BN output tiles in a static round-robin order over banded tiles.
@@ -38,7 +36,6 @@
 namespace ts {
 
 enum GemmEpi : int { EPI_BIAS = 0, EPI_GELU = 1, EPI_RESID = 2, EPI_QKV = 3, EPI_SWIGLU = 4 };
-enum GemmOperand : int { OPD_BF16 = 0, OPD_E4M3 = 1, OPD_S8 = 2 };   // element type of A and W
 
 
 struct GemmArgs {
@@ -46,8 +43,8 @@ struct GemmArgs {
   const float* bias;      // [N] or null
   bf16* out;              // [M, ldo]
   int ldo;
-  const float* a_scale;   // 8-bit only: [M] per-row scale of A
-  const float* w_scale;   // 8-bit only: [N] per-row scale of W
+  const float* a_scale;   // e4m3 only: [M] per-row scale of A
+  const float* w_scale;   // e4m3 only: [N] per-row scale of W
   // EPI_QKV
   int d;                  // model width: columns [0, d) q, [d, 2d) k, [2d, 3d) v
   const float* q_g;       // [64]
@@ -113,43 +110,25 @@ __device__ __forceinline__ void qk_norm_rope64(float* v, const float* __restrict
   }
 }
 
-// int32 accumulators (as the bits TMEM returned) to fp32; one rounding, at 2^-24
-template <int OPD, int N>
-__device__ __forceinline__ void gemm_acc_to_f32(float* v) {
-  if (OPD == OPD_S8) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = __int2float_rn(__float_as_int(v[i]));
-  }
-}
-// first of four columns whose scales and biases are read: integer products may end
-// inside a chunk, whose columns past N repeat the last four and are not stored
-template <int OPD>
-__device__ __forceinline__ int gemm_col4(int col, int n) {
-  return OPD == OPD_S8 ? min(col, n - 4) : col;
-}
-
-// Epilogue arithmetic of one 64-column chunk of a row held by this thread: 8-bit
+// Epilogue arithmetic of one 64-column chunk of a row held by this thread: e4m3
 // scales, bias, then GELU or QK-RMSNorm + RoPE (the residual is added by the caller).
-template <int EPI, int OPD, int R0, int R1, int R2>
+template <int EPI, bool FP8, int R0, int R1, int R2>
 __device__ __forceinline__ void gemm_epilogue64(float* v, int col, float rs, const int4 pos, const GemmArgs& args) {
-  constexpr bool Q8 = OPD != OPD_BF16;
-  gemm_acc_to_f32<OPD, 64>(v);
-  if (Q8 && args.bias) {
+  if (FP8 && args.bias) {
     // dequantisation scale and bias in one FMA per value
 #pragma unroll
     for (int i = 0; i < 64; i += 4) {
-      const int c = gemm_col4<OPD>(col + i, args.N);
-      const float4 ws = __ldg(reinterpret_cast<const float4*>(args.w_scale + c));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(args.bias + c));
+      const float4 ws = __ldg(reinterpret_cast<const float4*>(args.w_scale + col + i));
+      const float4 b = __ldg(reinterpret_cast<const float4*>(args.bias + col + i));
       v[i] = fmaf(v[i], rs * ws.x, b.x);
       v[i + 1] = fmaf(v[i + 1], rs * ws.y, b.y);
       v[i + 2] = fmaf(v[i + 2], rs * ws.z, b.z);
       v[i + 3] = fmaf(v[i + 3], rs * ws.w, b.w);
     }
-  } else if (Q8) {
+  } else if (FP8) {
 #pragma unroll
     for (int i = 0; i < 64; i += 4) {
-      const float4 ws = __ldg(reinterpret_cast<const float4*>(args.w_scale + gemm_col4<OPD>(col + i, args.N)));
+      const float4 ws = __ldg(reinterpret_cast<const float4*>(args.w_scale + col + i));
       v[i] *= rs * ws.x;
       v[i + 1] *= rs * ws.y;
       v[i + 2] *= rs * ws.z;
@@ -166,7 +145,7 @@ __device__ __forceinline__ void gemm_epilogue64(float* v, int col, float rs, con
     }
   }
   if (EPI == EPI_GELU) {
-    if (Q8) {
+    if (FP8) {
 #pragma unroll
       for (int i = 0; i < 64; i += 2) {
         const uint64_t y = gelu_erf_one_sfu2(pack_f32x2(v[i], v[i + 1]));
@@ -190,24 +169,21 @@ __device__ __forceinline__ void gemm_epilogue64(float* v, int col, float rs, con
 // SwiGLU of 32 outputs held by this thread: g (gate sums) is overwritten with
 // silu(g * sg + b_g) * (u * su + b_u); col is the output column of g[0], F the
 // output width (gate row col + i, up row F + col + i of W, bias and w_scale).
-template <int OPD>
-__device__ __forceinline__ void swiglu32(float* g, float* u, int col, int F, float rs, const GemmArgs& args) {
-  gemm_acc_to_f32<OPD, 32>(g);
-  gemm_acc_to_f32<OPD, 32>(u);
+template <bool FP8>
+__device__ __forceinline__ void swiglu32(float* g, const float* u, int col, int F, float rs, const GemmArgs& args) {
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
-    const int c = gemm_col4<OPD>(col + i, F);
     float gg[4] = {g[i], g[i + 1], g[i + 2], g[i + 3]};
     float uu[4] = {u[i], u[i + 1], u[i + 2], u[i + 3]};
-    if (OPD != OPD_BF16) {
-      const float4 wg = __ldg(reinterpret_cast<const float4*>(args.w_scale + c));
-      const float4 wu = __ldg(reinterpret_cast<const float4*>(args.w_scale + F + c));
+    if (FP8) {
+      const float4 wg = __ldg(reinterpret_cast<const float4*>(args.w_scale + col + i));
+      const float4 wu = __ldg(reinterpret_cast<const float4*>(args.w_scale + F + col + i));
       gg[0] *= rs * wg.x; gg[1] *= rs * wg.y; gg[2] *= rs * wg.z; gg[3] *= rs * wg.w;
       uu[0] *= rs * wu.x; uu[1] *= rs * wu.y; uu[2] *= rs * wu.z; uu[3] *= rs * wu.w;
     }
     if (args.bias) {
-      const float4 bg = __ldg(reinterpret_cast<const float4*>(args.bias + c));
-      const float4 bu = __ldg(reinterpret_cast<const float4*>(args.bias + F + c));
+      const float4 bg = __ldg(reinterpret_cast<const float4*>(args.bias + col + i));
+      const float4 bu = __ldg(reinterpret_cast<const float4*>(args.bias + F + col + i));
       gg[0] += bg.x; gg[1] += bg.y; gg[2] += bg.z; gg[3] += bg.w;
       uu[0] += bu.x; uu[1] += bu.y; uu[2] += bu.z; uu[3] += bu.w;
     }
@@ -248,7 +224,7 @@ __device__ __forceinline__ void gemm_tile_origin(int tile, int mt, int nt, int b
 // CTAs.  Each CTA's TMEM holds the accumulators of its own 128 rows, which its
 // epilogue warps read as in a single CTA; they release an accumulator on the even
 // CTA's barrier.  Half the W bytes per CTA leave room for deeper rings.
-template <int BN, int STAGES, int EPI, int OPD, int R0, int R1, int R2, int CG = 1>
+template <int BN, int STAGES, int EPI, bool FP8, int R0, int R1, int R2, int CG = 1>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmD, const GemmArgs args) {
@@ -256,10 +232,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   using SM = GemmSmem<BN, STAGES, CG>;
   constexpr int NMMA = 128 / 32;                  // MMAs per 128-byte K slice (32 bytes each)
   constexpr uint32_t TMEM_COLS = 2 * BN;          // two accumulators: 128, 256 or 512 columns
-  constexpr bool Q8 = OPD != OPD_BF16;
-  constexpr uint32_t IDESC = idesc_make(OPD == OPD_E4M3 ? 0u : 1u, BN, 128 * CG, OPD == OPD_S8 ? 2u : 1u);
+  constexpr uint32_t IDESC = idesc_make(FP8 ? 0u : 1u, BN, 128 * CG);
   constexpr int TM = 128 * CG;                    // output rows per tile
-  constexpr int KE = Q8 ? 128 : 64;              // K elements per slice
+  constexpr int KE = FP8 ? 128 : 64;              // K elements per slice
   constexpr bool GLU = EPI == EPI_SWIGLU;
   static_assert(!GLU || BN >= 128, "SwiGLU tiles need 64-column output chunks");
   constexpr int NCHUNK = GLU ? BN / 128 : BN / 64;   // 64-column output chunks per tile
@@ -277,9 +252,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int mt = (args.M + TM - 1) / TM;
-  const int nt = OPD == OPD_S8 ? (args.N + BN - 1) / BN : args.N / BN;
-  const int ntiles = mt * nt;
-  const int KB = OPD == OPD_S8 ? (args.K + KE - 1) / KE : args.K / KE;
+  const int ntiles = mt * (args.N / BN);
+  const int KB = args.K / KE;
   // tiles are walked per CTA, or per pair (the two CTAs of a pair walk the same tiles)
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const int unit = CG == 2 ? static_cast<int>(blockIdx.x) / 2 : static_cast<int>(blockIdx.x);
@@ -324,7 +298,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       bool ok = true;
       for (int tile = unit; tile < ntiles && ok; tile += units) {
         int m0, n0;
-        gemm_tile_origin(tile, mt, nt, BN, m0, n0, TM);
+        gemm_tile_origin(tile, mt, args.N / BN, BN, m0, n0, TM);
         for (int kb = 0; kb < KB; ++kb, ++it) {
           const uint32_t s = it % STAGES;
           if (it >= STAGES && !mbar_wait(bar_empty + 8 * s, ((it / STAGES) - 1) & 1)) { ok = false; break; }
@@ -371,16 +345,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           for (int k = 0; k < NMMA; ++k) {
             // +32 bytes of K = +2 in the descriptor's (address >> 4) field
             if (CG == 2) {
-              if (OPD == OPD_S8)
-                tc_mma_i8_pair(dt, da + 2 * k, db + 2 * k, IDESC, (kb | k) != 0);
-              else if (OPD == OPD_E4M3)
+              if (FP8)
                 tc_mma_f8_pair(dt, da + 2 * k, db + 2 * k, IDESC, (kb | k) != 0);
               else
                 tc_mma_f16_pair(dt, da + 2 * k, db + 2 * k, IDESC, (kb | k) != 0);
             } else {
-              if (OPD == OPD_S8)
-                tc_mma_i8(dt, da + 2 * k, db + 2 * k, IDESC, (kb | k) != 0);
-              else if (OPD == OPD_E4M3)
+              if (FP8)
                 tc_mma_f8(dt, da + 2 * k, db + 2 * k, IDESC, (kb | k) != 0);
               else
                 tc_mma_f16(dt, da + 2 * k, db + 2 * k, IDESC, (kb | k) != 0);
@@ -418,29 +388,27 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     for (int tile = unit; tile < ntiles; tile += units, ++j) {
       const uint32_t acc = j & 1, use = j >> 1;
       int m0, n0;
-      gemm_tile_origin(tile, mt, nt, BN, m0, n0, TM);
+      gemm_tile_origin(tile, mt, args.N / BN, BN, m0, n0, TM);
       m0 += static_cast<int>(rank) * 128;      // this CTA's rows of the tile
       const int row = m0 + quarter * 32 + lane;
       // the row's scale and coordinates are loaded while the accumulator fills
       float rs = 1.f;
-      if (Q8 && row < args.M) rs = __ldg(args.a_scale + row);
+      if (FP8 && row < args.M) rs = __ldg(args.a_scale + row);
       int4 pos = make_int4(0, 0, 0, 0);
       if (EPI == EPI_QKV && row < args.M) pos = __ldg(args.pos + row);
       if (!mbar_wait(bar_tfull + 8 * acc, use & 1)) break;
       tc_fence_after();
       const uint32_t trow = tmem + acc * BN + (static_cast<uint32_t>(quarter * 32) << 16);
-      // chunks that hold output columns (integer products may end inside a tile)
-      const int nchunk = OPD == OPD_S8 ? min(NCHUNK, ((GLU ? args.N / 2 - n0 / 2 : args.N - n0) + 63) / 64) : NCHUNK;
       int mine = 0;
 #pragma unroll 1
-      for (int c = half; c < nchunk; c += 2) ++mine;
+      for (int c = half; c < NCHUNK; c += 2) ++mine;
       if (mine == 0) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) release(acc);
       }
 #pragma unroll 1
-      for (int c = half, k = 0; c < nchunk; c += 2, ++k) {
+      for (int c = half, k = 0; c < NCHUNK; c += 2, ++k) {
         // the chunk goes out through this warp's 4 KB staging buffer (32 rows x 128 B,
         // 128-byte swizzle) as one TMA tile store; the residual comes in the same way
         if (store_pending) {
@@ -461,7 +429,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           float u[32];
           tmem_ld32(trow + BN / 2 + c * 64, u);
           tmem_wait_ld();
-          swiglu32<OPD>(v, u, col, args.N / 2, rs, args);
+          swiglu32<FP8>(v, u, col, args.N / 2, rs, args);
           tmem_ld32(trow + BN / 2 + c * 64 + 32, u);
           tmem_wait_ld();
           if (k == mine - 1) {         // last TMEM read of this warp for this tile
@@ -469,14 +437,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             __syncwarp();
             if (lane == 0) release(acc);
           }
-          swiglu32<OPD>(v + 32, u, col + 32, args.N / 2, rs, args);
+          swiglu32<FP8>(v + 32, u, col + 32, args.N / 2, rs, args);
         } else {
           if (k == mine - 1) {         // last TMEM read of this warp for this tile
             tc_fence_before();
             __syncwarp();
             if (lane == 0) release(acc);
           }
-          gemm_epilogue64<EPI, OPD, R0, R1, R2>(v, col, rs, pos, args);
+          gemm_epilogue64<EPI, FP8, R0, R1, R2>(v, col, rs, pos, args);
         }
         uint8_t* srow = smem + SM::EPI_OFFSET + warp * 4096 + lane * 128;
         if (EPI == EPI_RESID) {

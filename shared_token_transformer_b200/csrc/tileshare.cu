@@ -28,6 +28,7 @@
 #include "../../include/tileshare_ops.h"
 #include "attention.cuh"
 #include "common.cuh"
+#include "gemm_s8.cuh"
 #include "gemm_tc.cuh"
 #include "plan.inl"
 #include "rowops.cuh"
@@ -610,11 +611,11 @@ static ts_status run_quantize(ts_dtype dt, const void* x, int rows, int cols, ui
 // ---------------------------------------------------------------------------
 
 
-template <int BN, int STAGES, int EPI, int OPD, int R0, int R1, int R2, int CG = 1>
+template <int BN, int STAGES, int EPI, bool FP8, int R0, int R1, int R2, int CG = 1>
 static ts_status launch_gemm_tc(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& td,
                                 const ts::GemmArgs& args, cudaStream_t st) {
   using SM = ts::GemmSmem<BN, STAGES, CG>;
-  auto kern = ts::gemm_tc_kernel<BN, STAGES, EPI, OPD, R0, R1, R2, CG>;
+  auto kern = ts::gemm_tc_kernel<BN, STAGES, EPI, FP8, R0, R1, R2, CG>;
   static int configured[64] = {0};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -622,7 +623,7 @@ static ts_status launch_gemm_tc(const CUtensorMap& ta, const CUtensorMap& tb, co
     TS_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::LAUNCH_BYTES));
     configured[dev] = 1;
   }
-  const int tiles = ((args.M + 128 * CG - 1) / (128 * CG)) * ((args.N + BN - 1) / BN);
+  const int tiles = ((args.M + 128 * CG - 1) / (128 * CG)) * (args.N / BN);
   trace_pre(st);
   if (CG == 2) {
     // one pair per two SMs, both CTAs of a pair walking the same tiles
@@ -635,19 +636,19 @@ static ts_status launch_gemm_tc(const CUtensorMap& ta, const CUtensorMap& tb, co
   return trace_post(st, "gemm_tc");
 }
 
-template <int EPI, int OPD, int R0, int R1, int R2>
+template <int EPI, bool FP8, int R0, int R1, int R2>
 static ts_status dispatch_gemm_bn(int bn, bool pair, const CUtensorMap& ta, const CUtensorMap& tb,
                                   const CUtensorMap& td, const ts::GemmArgs& args, cudaStream_t st) {
   switch (bn) {
     case 256:
-      if (pair) return launch_gemm_tc<256, 6, EPI, OPD, R0, R1, R2, 2>(ta, tb, td, args, st);
-      return launch_gemm_tc<256, 4, EPI, OPD, R0, R1, R2>(ta, tb, td, args, st);
-    case 128: return launch_gemm_tc<128, 6, EPI, OPD, R0, R1, R2>(ta, tb, td, args, st);
+      if (pair) return launch_gemm_tc<256, 6, EPI, FP8, R0, R1, R2, 2>(ta, tb, td, args, st);
+      return launch_gemm_tc<256, 4, EPI, FP8, R0, R1, R2>(ta, tb, td, args, st);
+    case 128: return launch_gemm_tc<128, 6, EPI, FP8, R0, R1, R2>(ta, tb, td, args, st);
     default:
       if constexpr (EPI == ts::EPI_SWIGLU)   // SwiGLU tiles are at least 128 wide
-        return launch_gemm_tc<128, 6, EPI, OPD, R0, R1, R2>(ta, tb, td, args, st);
+        return launch_gemm_tc<128, 6, EPI, FP8, R0, R1, R2>(ta, tb, td, args, st);
       else
-        return launch_gemm_tc<64, 8, EPI, OPD, R0, R1, R2>(ta, tb, td, args, st);
+        return launch_gemm_tc<64, 8, EPI, FP8, R0, R1, R2>(ta, tb, td, args, st);
   }
 }
 
@@ -665,22 +666,21 @@ static bool gemm_pairs_enabled() {
 // Output tile width for the persistent GEMM: the persistent CTAs walk the tiles
 // round-robin, so the busiest CTA handles ceil(tiles / SMs) tiles.  Cost model:
 // that count times (BN + 48), 48 columns standing for the fixed per-tile work
-// (pipeline fill, epilogue tail); ties go to the wider tile.  ragged: the last
-// column tile may end past N (integer products).
-static int pick_bn(int M, int N, bool ragged = false) {
+// (pipeline fill, epilogue tail); ties go to the wider tile.
+static int pick_bn(int M, int N) {
   // tuning override: TS_GEMM_BN=64|128|256 forces the tile width where it divides N
   static const int forced = [] {
     const char* e = std::getenv("TS_GEMM_BN");
     return e ? std::atoi(e) : 0;
   }();
-  if ((forced == 64 || forced == 128 || forced == 256) && (ragged || N % forced == 0)) return forced;
+  if ((forced == 64 || forced == 128 || forced == 256) && N % forced == 0) return forced;
   const int mt = (M + 127) / 128;
   const int sms = num_sms();
   int best = 64;
   long best_cost = -1;
   for (int bn : {256, 128, 64}) {
-    if (N % bn && !ragged) continue;
-    const long tiles = static_cast<long>(mt) * ((N + bn - 1) / bn);
+    if (N % bn) continue;
+    const long tiles = static_cast<long>(mt) * (N / bn);
     const long cost = ((tiles + sms - 1) / sms) * (bn + 48);
     if (best_cost < 0 || cost < best_cost) {
       best = bn;
@@ -703,6 +703,123 @@ static ts_status check_gemm_sizes(const ts_model_desc* m, int K, int N) {
   return TS_OK;
 }
 
+// ---------------------------------------------------------------------------
+// 8-bit integer GEMM
+// ---------------------------------------------------------------------------
+// Output (and residual) map of the integer GEMM: boxes of 32 rows x cw columns, rows of 64 or 128 bytes swizzled alike.
+static ts_status make_tmap_box(CUtensorMap* map, void* base, int rows, int cols, int cw) {
+  EncodeTiledFn enc;
+  TS_TRY(encode_fn(&enc));
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(cw), 32};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, cw == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(TS_ERR_CUDA, "cuTensorMapEncodeTiled (output) failed (%d)", static_cast<int>(r));
+  return TS_OK;
+}
+
+template <int BN, int STAGES, int EPI, int R0, int R1, int R2, int CG>
+static ts_status launch_gemm_s8(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& td,
+                                const ts::GemmArgs& args, cudaStream_t st) {
+  using SM = ts::S8Smem<BN, STAGES, EPI, CG>;
+  auto kern = ts::gemm_s8_kernel<BN, STAGES, EPI, R0, R1, R2, CG>;
+  static int configured[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !configured[dev]) {
+    TS_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::LAUNCH_BYTES));
+    if (dev < 64) configured[dev] = 1;
+  }
+  const int tiles = ((args.M + 128 * CG - 1) / (128 * CG)) * ((args.N + BN - 1) / BN);
+  trace_pre(st);
+  if (CG == 2)
+    launch_pdl_pair(kern, dim3(2 * std::min(tiles, num_sms() / 2)), dim3(ts::kS8Threads), SM::LAUNCH_BYTES, st, ta, tb,
+                    td, args);
+  else
+    launch_pdl(kern, dim3(std::min(tiles, num_sms())), dim3(ts::kS8Threads), SM::LAUNCH_BYTES, st, ta, tb, td, args);
+  return trace_post(st, "gemm_s8");
+}
+
+template <int EPI, int R0, int R1, int R2>
+static ts_status dispatch_gemm_s8(int bn, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& td,
+                                  const ts::GemmArgs& args, cudaStream_t st) {
+  constexpr int STAGES = EPI == ts::EPI_QKV ? 4 : 5;    // boxes of a whole head take 32 KB more
+  if (bn == 256) return launch_gemm_s8<256, STAGES, EPI, R0, R1, R2, 2>(ta, tb, td, args, st);
+  if constexpr (EPI != ts::EPI_SWIGLU)   // SwiGLU tiles are at least 128 wide
+    if (bn == 64) return launch_gemm_s8<64, 6, EPI, R0, R1, R2, 1>(ta, tb, td, args, st);
+  return launch_gemm_s8<128, STAGES, EPI, R0, R1, R2, 1>(ta, tb, td, args, st);
+}
+
+// Tile of the integer GEMM: 256 x 256 by pairs of SMs, 128 x 128 or 128 x 64 by one.
+static int pick_bn_s8(int M, int N, int K, bool glu) {
+  static const int forced = [] {    // tuning override, as for the other GEMMs
+    const char* e = std::getenv("TS_GEMM_BN");
+    return e ? std::atoi(e) : 0;
+  }();
+  if (forced == 256 || forced == 128 || (forced == 64 && !glu)) return forced;
+  const int sms = num_sms(), kb = (K + 127) / 128;
+  struct Tile {
+    int bn, rows, units, slice, epi;
+  };
+  const Tile tiles[] = {{256, 256, sms / 2, 512, 2500}, {128, 128, sms, 512, 1500}, {64, 128, sms, 384, 1000}};
+  int best = 128;
+  long best_cost = -1;
+  for (const Tile& t : tiles) {
+    if (glu && t.bn == 64) continue;
+    const long n = static_cast<long>((M + t.rows - 1) / t.rows) * ((N + t.bn - 1) / t.bn);
+    const long cost = ((n + t.units - 1) / t.units) * std::max(kb * t.slice, t.epi) + t.epi;
+    if (best_cost < 0 || cost < best_cost) {
+      best = t.bn;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
+// Y[M, N] = epi(A[M, K] W[., K]^T) of signed bytes with their scales (EPI_SWIGLU: W has 2N rows).
+static ts_status run_gemm_s8(const ts_model_desc* m, int epi, const void* A, const float* a_scale, const void* W,
+                             const float* w_scale, int M, int N, int K, const float* bias, bf16* out,
+                             const ts_layer_weights* qk, const int* pos, cudaStream_t st, const ts::RopeTable& rt) {
+  const bool glu = epi == ts::EPI_SWIGLU;
+  const int NA = glu ? 2 * N : N;
+  const int bn = pick_bn_s8(M, NA, K, glu);
+  CUtensorMap ta, tb, td;
+  TS_TRY(make_tmap(&ta, A, M, K, 1, 128));
+  TS_TRY(make_tmap(&tb, W, NA, K, 1, (glu || bn == 256) ? bn / 2 : bn));
+  TS_TRY(make_tmap_box(&td, out, M, N, epi == ts::EPI_QKV ? 64 : 32));   // the epilogue's boxes (s8_box)
+  ts::GemmArgs g{};
+  g.M = M;
+  g.N = NA;
+  g.K = K;
+  g.bias = bias;
+  g.out = out;
+  g.ldo = N;
+  g.a_scale = a_scale;
+  g.w_scale = w_scale;
+  g.d = m->d;
+  g.eps_qk = m->eps_qk;
+  if (epi == ts::EPI_QKV) {
+    g.q_g = qk->q_g;
+    g.k_g = qk->k_g;
+    g.pos = reinterpret_cast<const int4*>(pos);
+    g.rope_cs = rt.cs;
+    for (int a = 0; a < 3; ++a) g.rope_off[a] = rt.off[a];
+  }
+  switch (epi) {
+    case ts::EPI_BIAS: return dispatch_gemm_s8<ts::EPI_BIAS, 0, 32, 32>(bn, ta, tb, td, g, st);
+    case ts::EPI_GELU: return dispatch_gemm_s8<ts::EPI_GELU, 0, 32, 32>(bn, ta, tb, td, g, st);
+    case ts::EPI_RESID: return dispatch_gemm_s8<ts::EPI_RESID, 0, 32, 32>(bn, ta, tb, td, g, st);
+    case ts::EPI_SWIGLU: return dispatch_gemm_s8<ts::EPI_SWIGLU, 0, 32, 32>(bn, ta, tb, td, g, st);
+    case ts::EPI_QKV:
+      return m->rope_dims[0] == 16 ? dispatch_gemm_s8<ts::EPI_QKV, 16, 24, 24>(bn, ta, tb, td, g, st)
+                                   : dispatch_gemm_s8<ts::EPI_QKV, 0, 32, 32>(bn, ta, tb, td, g, st);
+  }
+  return fail(TS_ERR_INVALID_ARG, "unknown epilogue");
+}
+
 // Y[M, N] = A[M, K] W[N, K]^T with epilogue; A bf16 (or 8-bit + a_scale), W bf16 (or 8-bit + w_scale).
 // EPI_SWIGLU: N is the output width and W, bias, w_scale have 2N rows (gate, then up).
 static ts_status run_gemm_tc(const char* name, const ts_model_desc* m, int epi, const void* A, const float* a_scale,
@@ -710,7 +827,7 @@ static ts_status run_gemm_tc(const char* name, const ts_model_desc* m, int epi, 
                              const ts_layer_weights* qk, const int* pos, cudaStream_t st,
                              const ts::RopeTable& rt = ts::RopeTable{}) {
   if (M == 0) return TS_OK;
-  const bool q8 = has_q8(m), s8 = m->dtype == TS_INT8;
+  const bool q8 = has_q8(m);
   const bool glu = epi == ts::EPI_SWIGLU;
   const int NA = glu ? 2 * N : N;   // accumulator columns = rows of W
   {
@@ -720,8 +837,9 @@ static ts_status run_gemm_tc(const char* name, const ts_model_desc* m, int epi, 
     set_work(name, 2.0 * M * static_cast<double>(NA) * K, bytes);
   }
   TS_TRY(check_gemm_sizes(m, K, N));
-  int bn = pick_bn(M, NA, s8);
-  if (glu && bn < 128) bn = 128;    // NA = 2N is a multiple of 128, or the last tile is clipped (int8)
+  if (m->dtype == TS_INT8) return run_gemm_s8(m, epi, A, a_scale, W, w_scale, M, N, K, bias, out, qk, pos, st, rt);
+  int bn = pick_bn(M, NA);
+  if (glu && bn < 128) bn = 128;    // NA = 2N is a multiple of 128
   // 256-wide tiles of tall GEMMs run as two-SM pairs of 256 x 256 tiles
   const bool pair = bn == 256 && M >= kGemmPairMinRows && gemm_pairs_enabled();
   CUtensorMap ta, tb, td;
@@ -748,9 +866,8 @@ static ts_status run_gemm_tc(const char* name, const ts_model_desc* m, int epi, 
   }
   const bool r3 = m->rope_dims[0] == 16;
 #define TS_GEMM_EPI(E, R0, R1, R2) \
-  (s8   ? dispatch_gemm_bn<E, ts::OPD_S8, R0, R1, R2>(bn, pair, ta, tb, td, g, st)     \
-   : q8 ? dispatch_gemm_bn<E, ts::OPD_E4M3, R0, R1, R2>(bn, pair, ta, tb, td, g, st)   \
-        : dispatch_gemm_bn<E, ts::OPD_BF16, R0, R1, R2>(bn, pair, ta, tb, td, g, st))
+  (q8 ? dispatch_gemm_bn<E, true, R0, R1, R2>(bn, pair, ta, tb, td, g, st)     \
+      : dispatch_gemm_bn<E, false, R0, R1, R2>(bn, pair, ta, tb, td, g, st))
   switch (epi) {
     case ts::EPI_BIAS: return TS_GEMM_EPI(ts::EPI_BIAS, 0, 32, 32);
     case ts::EPI_GELU: return TS_GEMM_EPI(ts::EPI_GELU, 0, 32, 32);
