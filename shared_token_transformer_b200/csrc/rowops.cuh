@@ -181,7 +181,15 @@ __global__ void __launch_bounds__(256) layernorm_generic_kernel(const T* __restr
 //   x' = x + gate[group(r)] * scale * Norm_post(y),   xn = Norm_pre(x')
 // with either norm, the gate and the scale optional.  Both norms are LayerNorm
 // (population variance, two passes over the row in registers) or, with rms set,
-// RMSNorm.  x' enters the second norm unrounded.  One warp per row.
+// RMSNorm.  x' enters the second norm unrounded.
+//
+// Bound by DRAM: a row of x and of y read, of x' and of xn written.  What keeps a kernel
+// from that bound is the work beside the bytes, so it is shared by as many columns as
+// registers allow: a team of one warp (two for wide rows, more where only that divides
+// the row) takes two rows at a time, NV 16-byte vectors of each in a thread, and each
+// reduction, barrier and read of the gains and biases in shared memory serves both rows.
+// Rows arrive by bulk copy without registers; the copy of the next y starts when this
+// one is in registers, that of the next x when x' is formed.
 // ---------------------------------------------------------------------------
 struct NormGateArgs {
   int rows, d, groups, rms;
@@ -207,85 +215,482 @@ __device__ __forceinline__ int norm_gate_group(const NormGateArgs& a, size_t row
   return g;
 }
 
-// normalise a row held by a warp in place: (v - mean) * rstd * g + b
-template <typename T, int NV>
-__device__ __forceinline__ void norm_row(float (&v)[NV][Vec<T>::E], int lane, int d, const float* g, const float* b,
-                                         float eps, int rms) {
-  constexpr int E = Vec<T>::E;
-  float s = 0.f;
+// E values in 16 bytes as packed pairs, and back
+template <typename T>
+__device__ __forceinline__ void unpack_pairs(const uint4& u, uint64_t (&p)[Vec<T>::E / 2]);
+template <>
+__device__ __forceinline__ void unpack_pairs<bf16>(const uint4& u, uint64_t (&p)[4]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int e = 0; e < E; ++e) s += v[i][e];
-  const float mean = rms ? 0.f : warp_sum(s) / d;
-  float q = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float c = v[i][e] - mean;
-      q = fmaf(c, c, q);
+  for (int i = 0; i < 4; ++i) p[i] = pack_f32x2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ void unpack_pairs<float>(const uint4& u, uint64_t (&p)[2]) {
+  p[0] = pack_f32x2(__uint_as_float(u.x), __uint_as_float(u.y));
+  p[1] = pack_f32x2(__uint_as_float(u.z), __uint_as_float(u.w));
+}
+__device__ __forceinline__ uint4 pack_pairs(const uint64_t (&p)[4]) {
+  return make_uint4(pack_bf16(lo_f32(p[0]), hi_f32(p[0])), pack_bf16(lo_f32(p[1]), hi_f32(p[1])),
+                    pack_bf16(lo_f32(p[2]), hi_f32(p[2])), pack_bf16(lo_f32(p[3]), hi_f32(p[3])));
+}
+__device__ __forceinline__ uint4 pack_pairs(const uint64_t (&p)[2]) {
+  return make_uint4(__float_as_uint(lo_f32(p[0])), __float_as_uint(hi_f32(p[0])), __float_as_uint(lo_f32(p[1])),
+                    __float_as_uint(hi_f32(p[1])));
+}
+// A row's 8-bit form from its largest magnitude (as bits), and the bytes of 2 P values held as pairs.
+template <int Q8>
+struct RowCode {
+  RowQuantS8 s8;
+  float e_scale, e_inv;
+  __device__ __forceinline__ explicit RowCode(uint32_t amax) {
+    if (Q8 == ROW_S8) {
+      s8 = row_quant_s8(amax);
+    } else {
+      const float m = __uint_as_float(amax);
+      e_scale = m > 0.f ? m / 448.0f : 1.0f;
+      e_inv = 1.0f / e_scale;
     }
-  const float rstd = rsqrtf(warp_sum(q) / d + eps);
+  }
+  __device__ __forceinline__ float scale() const { return Q8 == ROW_S8 ? s8.scale : e_scale; }
+  template <int P>
+  __device__ __forceinline__ void put(const uint64_t (&v)[P], uint8_t* dst) const {
+    uint32_t w[P / 2];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c0 = (i * 32 + lane) * E;
+    for (int j = 0; j < P / 2; ++j) {
+      const uint64_t p = v[2 * j], q = v[2 * j + 1];
+      if (Q8 == ROW_S8)
+        w[j] = quant_s8x4(lo_f32(p), hi_f32(p), lo_f32(q), hi_f32(q), s8);
+      else
+        w[j] = f32x2_to_e4m3x2(lo_f32(p) * e_inv, hi_f32(p) * e_inv) |
+               (static_cast<uint32_t>(f32x2_to_e4m3x2(lo_f32(q) * e_inv, hi_f32(q) * e_inv)) << 16);
+    }
+    if (P == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[P / 2 - 1]);
+    else
+      *reinterpret_cast<uint32_t*>(dst) = w[0];
+  }
+};
+
+// Few rows: a block of d / E threads (E columns each) takes two rows at a time, with its
+// columns' gains, biases and gates in registers; what counts is the chain of loads and
+// reductions of one pair.  1 x 1536 takes 3.0 us against 4.2 us by norm_gate_kernel,
+// 512 x 1536 3.7 against 6.4 us; from about two pairs a block on the latter is faster
+// (4000 x 1536: 16.5 us against 20).
+template <typename T, int Q8>
+__global__ void __launch_bounds__(256) norm_gate_few_kernel(const T* x, const T* y, T* x_out, T* xn, uint8_t* q8,
+                                                            float* qscale, const NormGateArgs a) {
+  __shared__ __align__(16) float red[2][2][8];
+  constexpr int E = Vec<T>::E, P = E / 2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = threadIdx.x * E;
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  if (threadIdx.x < 32) (&red[0][0][0])[threadIdx.x] = 0.f;    // warps that a block lacks add nothing
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  auto pairs_of = [&](const float* v, float fill, uint64_t (&p)[P]) {   // this thread's columns of a vector
 #pragma unroll
-    for (int e = 0; e < E; e += 4) {
-      const float4 gg = __ldg(reinterpret_cast<const float4*>(g + c0 + e));
-      const float4 bb = rms ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldg(reinterpret_cast<const float4*>(b + c0 + e));
-      v[i][e] = (v[i][e] - mean) * rstd * gg.x + bb.x;
-      v[i][e + 1] = (v[i][e + 1] - mean) * rstd * gg.y + bb.y;
-      v[i][e + 2] = (v[i][e + 2] - mean) * rstd * gg.z + bb.z;
-      v[i][e + 3] = (v[i][e + 3] - mean) * rstd * gg.w + bb.w;
+    for (int i = 0; i < P; i += 2) {
+      const float4 f = v ? __ldg(reinterpret_cast<const float4*>(v + c0 + 2 * i)) : make_float4(fill, fill, fill, fill);
+      p[i] = pack_f32x2(f.x, f.y);
+      p[i + 1] = pack_f32x2(f.z, f.w);
+    }
+  };
+  uint64_t post_g[P], post_b[P], pre_g[P], pre_b[P], scale[P], gs[P];
+  pairs_of(a.post_g, 1.f, post_g);
+  pairs_of(a.rms ? nullptr : a.post_b, 0.f, post_b);
+  pairs_of(a.pre_g, 1.f, pre_g);
+  pairs_of(a.rms ? nullptr : a.pre_b, 0.f, pre_b);
+  pairs_of(a.scale, 1.f, scale);
+  int gs_group = -1;
+  auto load_gate = [&](int group) {        // gate * scale of a group
+    pairs_of(a.gate ? a.gate + static_cast<size_t>(group) * a.d : nullptr, 1.f, gs);
+#pragma unroll
+    for (int i = 0; i < P; ++i) gs[i] = mul_f32x2(gs[i], scale[i]);
+    gs_group = group;
+  };
+  int rb = 0;                              // reduction buffer: a buffer's next use is two barriers away
+  auto sum2 = [&](float& s0, float& s1) {  // (s0, s1) of every thread -> their sums over the block
+    float m = lane < 16 ? s0 : s1;
+    m += __shfl_xor_sync(0xffffffffu, lane < 16 ? s1 : s0, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+    if ((lane & 15) == 0) red[rb][lane >> 4][warp] = m;
+    __syncthreads();
+    const float4* r = reinterpret_cast<const float4*>(&red[rb][0][0]);
+    const float4 a0 = r[0], a1 = r[1], b0 = r[2], b1 = r[3];
+    s0 = ((a0.x + a0.y) + (a0.z + a0.w)) + ((a1.x + a1.y) + (a1.z + a1.w));
+    s1 = ((b0.x + b0.y) + (b0.z + b0.w)) + ((b1.x + b1.y) + (b1.z + b1.w));
+    rb ^= 1;
+  };
+  auto max2 = [&](uint32_t& s0, uint32_t& s1) {
+    s0 = warp_max_u32(s0);
+    s1 = warp_max_u32(s1);
+    if (lane == 0) {
+      red[rb][0][warp] = __uint_as_float(s0);
+      red[rb][1][warp] = __uint_as_float(s1);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      s0 = max(s0, __float_as_uint(red[rb][0][w]));
+      s1 = max(s1, __float_as_uint(red[rb][1][w]));
+    }
+    rb ^= 1;
+  };
+  auto norm2 = [&](uint64_t (&v0)[P], uint64_t (&v1)[P], const uint64_t (&g)[P], const uint64_t (&b)[P]) {
+    if (!a.rms) {
+      uint64_t t0 = 0ull, t1 = 0ull;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        t0 = add_f32x2(t0, v0[i]);
+        t1 = add_f32x2(t1, v1[i]);
+      }
+      float s0 = lo_f32(t0) + hi_f32(t0), s1 = lo_f32(t1) + hi_f32(t1);
+      sum2(s0, s1);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        v0[i] = add_f32x2(v0[i], splat_f32x2(-s0 * inv_d));
+        v1[i] = add_f32x2(v1[i], splat_f32x2(-s1 * inv_d));
+      }
+    }
+    uint64_t t0 = 0ull, t1 = 0ull;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      t0 = fma_f32x2(v0[i], v0[i], t0);
+      t1 = fma_f32x2(v1[i], v1[i], t1);
+    }
+    float q0 = lo_f32(t0) + hi_f32(t0), q1 = lo_f32(t1) + hi_f32(t1);
+    sum2(q0, q1);
+    const uint64_t r0 = splat_f32x2(rsqrtf(q0 * inv_d + a.eps)), r1 = splat_f32x2(rsqrtf(q1 * inv_d + a.eps));
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      v0[i] = fma_f32x2(mul_f32x2(v0[i], r0), g[i], b[i]);
+      v1[i] = fma_f32x2(mul_f32x2(v1[i], r1), g[i], b[i]);
+    }
+  };
+  const size_t rows = a.rows;
+  for (size_t row = 2 * static_cast<size_t>(blockIdx.x); row < rows; row += 2 * static_cast<size_t>(gridDim.x)) {
+    const bool two = row + 1 < rows;
+    const size_t o0 = row * a.d + c0, o1 = two ? o0 + a.d : o0;
+    uint64_t x0[P], x1[P], v0[P], v1[P];
+    unpack_pairs<T>(*reinterpret_cast<const uint4*>(y + o0), v0);
+    unpack_pairs<T>(*reinterpret_cast<const uint4*>(y + o1), v1);
+    unpack_pairs<T>(*reinterpret_cast<const uint4*>(x + o0), x0);
+    unpack_pairs<T>(*reinterpret_cast<const uint4*>(x + o1), x1);
+    const int g0 = norm_gate_group(a, row), g1 = two ? norm_gate_group(a, row + 1) : -1;
+    if (g0 >= 0 && g0 != gs_group) load_gate(g0);
+    if (a.post_g) norm2(v0, v1, post_g, post_b);
+#pragma unroll
+    for (int i = 0; i < P; ++i) v0[i] = fma_f32x2(gs[i], v0[i], x0[i]);
+    if (g1 >= 0 && g1 != gs_group) load_gate(g1);
+#pragma unroll
+    for (int i = 0; i < P; ++i) v1[i] = fma_f32x2(gs[i], v1[i], x1[i]);
+    if (g0 >= 0) *reinterpret_cast<uint4*>(x_out + o0) = pack_pairs(v0);
+    if (g1 >= 0) *reinterpret_cast<uint4*>(x_out + o1) = pack_pairs(v1);
+    if (!a.pre_g) continue;
+    norm2(v0, v1, pre_g, pre_b);
+    if (Q8 == ROW_T) {
+      if (g0 >= 0) *reinterpret_cast<uint4*>(xn + o0) = pack_pairs(v0);
+      if (g1 >= 0) *reinterpret_cast<uint4*>(xn + o1) = pack_pairs(v1);
+    } else {
+      uint32_t m0 = 0, m1 = 0;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        m0 = max(m0, max(abs_bits(lo_f32(v0[i])), abs_bits(hi_f32(v0[i]))));
+        m1 = max(m1, max(abs_bits(lo_f32(v1[i])), abs_bits(hi_f32(v1[i]))));
+      }
+      max2(m0, m1);
+      const RowCode<Q8> r0(m0), r1(m1);
+      if (g0 >= 0) {
+        if (threadIdx.x == 0) qscale[row] = r0.scale();
+        r0.template put<P>(v0, q8 + o0);
+      }
+      if (g1 >= 0) {
+        if (threadIdx.x == 0) qscale[row + 1] = r1.scale();
+        r1.template put<P>(v1, q8 + o1);
+      }
     }
   }
 }
 
+constexpr int kNormGateTeamWarps = 8;    // most warps of a team
+constexpr int kNormGateTeams = 32;       // most teams of a block
+constexpr int kNormGateStages = 4;       // most pairs of rows on their way to a team
+// most threads of a block by the registers that NV vectors of two rows take
+template <int NV>
+constexpr int norm_gate_threads() {
+  return NV == 1 ? 896 : NV == 2 ? 640 : NV == 3 ? 512 : 384;
+}
+
 template <typename T, int NV, int Q8>
-__global__ void __launch_bounds__(256) norm_gate_kernel(const T* x, const T* y, T* x_out, T* xn, uint8_t* q8,
-                                                        float* qscale, const NormGateArgs a) {
+__global__ void __launch_bounds__(norm_gate_threads<NV>(), 1)
+    norm_gate_kernel(const T* x, const T* y, T* x_out, T* xn, uint8_t* q8, float* qscale, const NormGateArgs a,
+                     int team_warps, int stages) {
+  extern __shared__ __align__(128) uint8_t smem[];    // vectors [4][d], then per team stages x (2 rows of y, 2 of x)
+  __shared__ __align__(16) float red[kNormGateTeams][2][2][kNormGateTeamWarps];
+  __shared__ __align__(8) uint64_t bars[kNormGateTeams][kNormGateStages][2];    // y, x
+  constexpr int E = Vec<T>::E, P = E / 2, Q = E / 4;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % team_warps, team = (threadIdx.x >> 5) / team_warps;
+  const int tsize = 32 * team_warps, t = threadIdx.x - team * tsize, teams = blockDim.x / tsize;
+  const uint32_t rowbytes = static_cast<uint32_t>(a.d) * sizeof(T);
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  uint8_t* ring = smem + static_cast<size_t>(16) * a.d + static_cast<size_t>(team) * stages * 4 * rowbytes;
+  if (t == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(smem_u32(&bars[team][s][0]), 1);
+      mbar_init(smem_u32(&bars[team][s][1]), 1);
+    }
+    fence_barrier_init();
+  }
+  if (t < 32) (&red[team][0][0][0])[t] = 0.f;    // warps that a team lacks add nothing
+  // whether a flag holds in all threads of the team, and a barrier of them
+  auto team_all = [&](bool f) -> bool {
+    if (team_warps == 1) return __all_sync(0xffffffffu, f);
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(r)
+        : "r"(f ? 1u : 0u), "r"(1 + team), "r"(tsize)
+        : "memory");
+    return r != 0;
+  };
+  team_all(true);
   pdl_wait();
   pdl_trigger();
-  constexpr int E = Vec<T>::E;
-  const int lane = threadIdx.x & 31;
-  const size_t step = static_cast<size_t>(gridDim.x) * (blockDim.x >> 5);
-  for (size_t row = static_cast<size_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-       row < static_cast<size_t>(a.rows); row += step) {
-    const int group = norm_gate_group(a, row);
-    if (group < 0) continue;
-    float v[NV][E];
-    uint4 raw[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) raw[i] = *reinterpret_cast<const uint4*>(x + row * a.d + (i * 32 + lane) * E);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) Vec<T>::load(y + row * a.d + (i * 32 + lane) * E, v[i]);
-    if (a.post_g) norm_row<T, NV>(v, lane, a.d, a.post_g, a.post_b, a.eps, a.rms);
-    const float* gate = a.gate ? a.gate + static_cast<size_t>(group) * a.d : nullptr;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float r[E];
-      Vec<T>::load(reinterpret_cast<const T*>(&raw[i]), r);
-      const int c0 = (i * 32 + lane) * E;
-#pragma unroll
-      for (int e = 0; e < E; e += 4) {
-        float4 k = gate ? __ldg(reinterpret_cast<const float4*>(gate + c0 + e)) : make_float4(1.f, 1.f, 1.f, 1.f);
-        if (a.scale) {
-          const float4 s = __ldg(reinterpret_cast<const float4*>(a.scale + c0 + e));
-          k.x *= s.x; k.y *= s.y; k.z *= s.z; k.w *= s.w;
-        }
-        v[i][e] = fmaf(k.x, v[i][e], r[e]);
-        v[i][e + 1] = fmaf(k.y, v[i][e + 1], r[e + 1]);
-        v[i][e + 2] = fmaf(k.z, v[i][e + 2], r[e + 2]);
-        v[i][e + 3] = fmaf(k.w, v[i][e + 3], r[e + 3]);
-      }
-      Vec<T>::store(x_out + row * a.d + c0, v[i]);
+  const size_t rows = a.rows, step = 2 * static_cast<size_t>(gridDim.x) * teams;
+  size_t row = 2 * (static_cast<size_t>(blockIdx.x) * teams + team);
+  // copy of a pair of rows of y (k = 0) or x (k = 1) into stage s, by one thread of the team
+  auto issue = [&](int s, int k, size_t r) {
+    const uint32_t n = r + 1 < rows ? 2 * rowbytes : rowbytes, bar = smem_u32(&bars[team][s][k]);
+    mbar_expect_tx(bar, n);
+    bulk_load(smem_u32(ring) + static_cast<uint32_t>(4 * s + 2 * k) * rowbytes, (k ? x : y) + r * a.d, n, bar);
+  };
+  if (t == 0)
+    for (int s = 0; s < stages && row + s * step < rows; ++s) {
+      issue(s, 0, row + s * step);
+      issue(s, 1, row + s * step);
     }
-    if (a.pre_g) {
-      norm_row<T, NV>(v, lane, a.d, a.pre_g, a.pre_b, a.eps, a.rms);
-      store_row<T, NV, Q8>(v, lane, xn, q8, qscale, row, a.d);
+  // The shared vectors.  Thread t owns vectors i * tsize + t of a row; the four-column quads of a vector lie tsize
+  // float4s apart, so that a warp reads them without bank conflicts.
+  const float* src[4] = {a.post_g, a.rms ? nullptr : a.post_b, a.pre_g, a.rms ? nullptr : a.pre_b};
+  float4* vecs = reinterpret_cast<float4*>(smem);
+  const int quads = a.d / 4;
+  for (int m0 = team; m0 < 4 * NV * Q; m0 += 8 * teams) {      // the teams take turns, eight loads in flight
+    float4 f[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int m = m0 + u * teams, k = m / (NV * Q), c = m % (NV * Q);
+      const float* v = k == 0 ? src[0] : k == 1 ? src[1] : k == 2 ? src[2] : src[3];
+      f[u] = m < 4 * NV * Q && v ? __ldg(reinterpret_cast<const float4*>(v) + (c / Q * tsize + t) * Q + c % Q)
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int m = m0 + u * teams;
+      if (m < 4 * NV * Q) vecs[m / (NV * Q) * quads + m % (NV * Q) * tsize + t] = f[u];
     }
   }
+  uint64_t gs[NV][P];                      // gate * scale of this thread's columns, for the group gs_group
+  int gs_group = -1;
+  auto load_gate = [&](int group) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < Q; ++j) {
+        const size_t c = static_cast<size_t>(i * tsize + t) * E + 4 * j;
+        float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
+        if (a.gate) f = __ldg(reinterpret_cast<const float4*>(a.gate + static_cast<size_t>(group) * a.d + c));
+        if (a.scale) {
+          const float4 sc = __ldg(reinterpret_cast<const float4*>(a.scale + c));
+          f.x *= sc.x; f.y *= sc.y; f.z *= sc.z; f.w *= sc.w;
+        }
+        gs[i][2 * j] = pack_f32x2(f.x, f.y);
+        gs[i][2 * j + 1] = pack_f32x2(f.z, f.w);
+      }
+    gs_group = group;
+  };
+  if (row < rows) {
+    const int g = norm_gate_group(a, row);
+    if (g >= 0) load_gate(g);
+  }
+  __syncthreads();
+  int rb = 0;                              // reduction buffer: a buffer's next use is two barriers away
+  // (s0, s1) of every thread -> their sums over the team; returns `flag` as team_all gives it
+  auto sum2 = [&](float& s0, float& s1, bool flag) -> bool {
+    float m = lane < 16 ? s0 : s1;
+    m += __shfl_xor_sync(0xffffffffu, lane < 16 ? s1 : s0, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+    if (team_warps == 1) {
+      const float other = __shfl_xor_sync(0xffffffffu, m, 16);
+      s0 = lane < 16 ? m : other;
+      s1 = lane < 16 ? other : m;
+      return __all_sync(0xffffffffu, flag);
+    }
+    if ((lane & 15) == 0) red[team][rb][lane >> 4][warp] = m;
+    const bool all = team_all(flag);
+    const float4* r = reinterpret_cast<const float4*>(&red[team][rb][0][0]);
+    const float4 a0 = r[0], a1 = r[1], b0 = r[2], b1 = r[3];
+    s0 = ((a0.x + a0.y) + (a0.z + a0.w)) + ((a1.x + a1.y) + (a1.z + a1.w));
+    s1 = ((b0.x + b0.y) + (b0.z + b0.w)) + ((b1.x + b1.y) + (b1.z + b1.w));
+    rb ^= 1;
+    return all;
+  };
+  auto max2 = [&](uint32_t& s0, uint32_t& s1) {
+    s0 = warp_max_u32(s0);
+    s1 = warp_max_u32(s1);
+    if (team_warps == 1) return;
+    if (lane == 0) {
+      red[team][rb][0][warp] = __uint_as_float(s0);
+      red[team][rb][1][warp] = __uint_as_float(s1);
+    }
+    team_all(true);
+    const uint4* r = reinterpret_cast<const uint4*>(&red[team][rb][0][0]);
+    const uint4 a0 = r[0], a1 = r[1], b0 = r[2], b1 = r[3];
+    s0 = max(max(max(a0.x, a0.y), max(a0.z, a0.w)), max(max(a1.x, a1.y), max(a1.z, a1.w)));
+    s1 = max(max(max(b0.x, b0.y), max(b0.z, b0.w)), max(max(b1.x, b1.y), max(b1.z, b1.w)));
+    rb ^= 1;
+  };
+  typedef uint64_t Row[NV][P];
+  auto total = [&](const Row& v) -> float {
+    uint64_t u = 0ull;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int p = 0; p < P; p += 2) u = add_f32x2(u, add_f32x2(v[i][p], v[i][p + 1]));
+    return lo_f32(u) + hi_f32(u);
+  };
+  auto squares = [&](const Row& v) -> float {
+    uint64_t u = 0ull, w = 0ull;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int p = 0; p < P; p += 2) {
+        u = fma_f32x2(v[i][p], v[i][p], u);
+        w = fma_f32x2(v[i][p + 1], v[i][p + 1], w);
+      }
+    u = add_f32x2(u, w);
+    return lo_f32(u) + hi_f32(u);
+  };
+  // both rows: v -> (v - mean) * rstd * g + b with g, b the shared vectors k, k + 1; the last barrier carries `flag`
+  auto norm2 = [&](Row& v0, Row& v1, int k, bool flag) -> bool {
+    if (!a.rms) {
+      float s0 = total(v0), s1 = total(v1);
+      sum2(s0, s1, true);
+      const uint64_t m0 = splat_f32x2(-s0 * inv_d), m1 = splat_f32x2(-s1 * inv_d);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          v0[i][p] = add_f32x2(v0[i][p], m0);
+          v1[i][p] = add_f32x2(v1[i][p], m1);
+        }
+    }
+    float q0 = squares(v0), q1 = squares(v1);
+    const bool all = sum2(q0, q1, flag);
+    const uint64_t r0 = splat_f32x2(rsqrtf(q0 * inv_d + a.eps)), r1 = splat_f32x2(rsqrtf(q1 * inv_d + a.eps));
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < Q; ++j) {
+        const float4 g = vecs[k * quads + (i * Q + j) * tsize + t], b = vecs[(k + 1) * quads + (i * Q + j) * tsize + t];
+        const uint64_t g0 = pack_f32x2(g.x, g.y), g1 = pack_f32x2(g.z, g.w), b0 = pack_f32x2(b.x, b.y),
+                       b1 = pack_f32x2(b.z, b.w);
+        v0[i][2 * j] = fma_f32x2(mul_f32x2(v0[i][2 * j], r0), g0, b0);
+        v1[i][2 * j] = fma_f32x2(mul_f32x2(v1[i][2 * j], r1), g0, b0);
+        v0[i][2 * j + 1] = fma_f32x2(mul_f32x2(v0[i][2 * j + 1], r0), g1, b1);
+        v1[i][2 * j + 1] = fma_f32x2(mul_f32x2(v1[i][2 * j + 1], r1), g1, b1);
+      }
+    return all;
+  };
+  auto put = [&](T* out, size_t r, const Row& v) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      *reinterpret_cast<uint4*>(out + r * a.d + static_cast<size_t>(i * tsize + t) * E) = pack_pairs(v[i]);
+  };
+  int s = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  for (; row < rows; row += step) {
+    const int g0 = norm_gate_group(a, row), g1 = row + 1 < rows ? norm_gate_group(a, row + 1) : -1;
+    const bool more = row + stages * step < rows;
+    const uint8_t* ys = ring + static_cast<size_t>(4 * s) * rowbytes + t * 16;
+    const uint8_t* xs = ys + 2 * static_cast<size_t>(rowbytes);
+    // both copies are waited for here, so that one barrier tells the team whether either gave up
+    const bool here = mbar_wait(smem_u32(&bars[team][s][0]), phase) && mbar_wait(smem_u32(&bars[team][s][1]), phase);
+    Row v0, v1;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      unpack_pairs<T>(*reinterpret_cast<const uint4*>(ys + i * tsize * 16), v0[i]);
+      unpack_pairs<T>(*reinterpret_cast<const uint4*>(ys + rowbytes + i * tsize * 16), v1[i]);
+    }
+    fence_proxy_async_smem();
+    ok = team_all(here);                   // and every thread has read y
+    if (!ok) break;
+    if (more && t == 0) issue(s, 0, row + stages * step);
+    if (a.post_g) norm2(v0, v1, 0, true);
+    if (g0 >= 0 && g0 != gs_group) load_gate(g0);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      uint64_t r[P];
+      unpack_pairs<T>(*reinterpret_cast<const uint4*>(xs + i * tsize * 16), r);
+#pragma unroll
+      for (int p = 0; p < P; ++p) v0[i][p] = fma_f32x2(gs[i][p], v0[i][p], r[p]);
+    }
+    if (g1 >= 0 && g1 != gs_group) load_gate(g1);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      uint64_t r[P];
+      unpack_pairs<T>(*reinterpret_cast<const uint4*>(xs + rowbytes + i * tsize * 16), r);
+#pragma unroll
+      for (int p = 0; p < P; ++p) v1[i][p] = fma_f32x2(gs[i][p], v1[i][p], r[p]);
+    }
+    fence_proxy_async_smem();
+    team_all(true);                        // every thread has read x
+    if (more && t == 0) issue(s, 1, row + stages * step);
+    if (g0 >= 0) put(x_out, row, v0);
+    if (g1 >= 0) put(x_out, row + 1, v1);
+    if (a.pre_g) {
+      norm2(v0, v1, 2, true);
+      if (Q8 == ROW_T) {
+        if (g0 >= 0) put(xn, row, v0);
+        if (g1 >= 0) put(xn, row + 1, v1);
+      } else {
+        uint32_t m0 = 0, m1 = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            m0 = max(m0, max(abs_bits(lo_f32(v0[i][p])), abs_bits(hi_f32(v0[i][p]))));
+            m1 = max(m1, max(abs_bits(lo_f32(v1[i][p])), abs_bits(hi_f32(v1[i][p]))));
+          }
+        max2(m0, m1);
+        auto put8 = [&](size_t r, const Row& v, uint32_t amax) {
+          const RowCode<Q8> code(amax);
+          if (t == 0) qscale[r] = code.scale();
+#pragma unroll
+          for (int i = 0; i < NV; ++i) code.template put<P>(v[i], q8 + r * a.d + static_cast<size_t>(i * tsize + t) * E);
+        };
+        if (g0 >= 0) put8(row, v0, m0);
+        if (g1 >= 0) put8(row + 1, v1, m1);
+      }
+    }
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+  // no copy may still be landing when the block exits (matters only after a timeout)
+  if (!ok)
+    for (int k = 0; k < stages && row + k * step < rows; ++k) {
+      mbar_wait(smem_u32(&bars[team][s][0]), phase);
+      mbar_wait(smem_u32(&bars[team][s][1]), phase);
+      if (++s == stages) {
+        s = 0;
+        phase ^= 1;
+      }
+    }
 }
 
 // any d (fp32 rows): one warp per row, scalar.  Only the lane that holds a column
@@ -621,7 +1026,9 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const bf16* __restri
 
 // ---------------------------------------------------------------------------
 // Per-row quantisation of a bf16 matrix to signed 8-bit integers (row_quant_s8).
-// cols % 8 == 0.  One warp per row, the second pass reads the row again.
+// cols % 8 == 0.  T threads share a row and hold it in registers between the maximum
+// and the rounding (NV 16-byte vectors each), so it is read once: bound by DRAM, 2
+// bytes read and 1 written per element.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t bf16x8_abs_bits(const uint4& u) {   // largest magnitude of 8 bf16, as fp32 bits
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -636,20 +1043,59 @@ __device__ __forceinline__ uint2 bf16x8_to_s8(const uint4& u, const RowQuantS8& 
   return make_uint2(quant_s8x4(f[0], f[1], f[2], f[3], r), quant_s8x4(f[4], f[5], f[6], f[7], r));
 }
 
-__global__ void __launch_bounds__(256) quantize_rows_s8_kernel(const bf16* __restrict__ x, int rows, int cols,
-                                                               uint8_t* __restrict__ q, float* __restrict__ scale) {
+template <int T, int NV>
+__global__ void __launch_bounds__(T > 128 ? T : 128) quantize_rows_s8_kernel(const bf16* __restrict__ x, int rows, int cols,
+                                                                            uint8_t* __restrict__ q,
+                                                                            float* __restrict__ scale) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const size_t row = static_cast<size_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (row >= static_cast<size_t>(rows)) return;
-  const bf16* xr = x + row * cols;
+  constexpr int RPB = T > 128 ? 1 : 128 / T;       // rows per block
+  const int t = threadIdx.x % T, nvec = cols / 8;
+  const size_t row = static_cast<size_t>(blockIdx.x) * RPB + threadIdx.x / T;
+  if (T < 128 && row >= static_cast<size_t>(rows)) return;   // whole warps; with T >= 128 a block is a row
+  const uint4* xr = reinterpret_cast<const uint4*>(x + row * cols);
+  uint4 v[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i] = t + i * T < nvec ? xr[t + i * T] : make_uint4(0, 0, 0, 0);
   uint32_t amax = 0;
-  for (int c = lane * 8; c < cols; c += 256) amax = max(amax, bf16x8_abs_bits(*reinterpret_cast<const uint4*>(xr + c)));
-  const RowQuantS8 r = row_quant_s8(warp_max_u32(amax));
-  if (lane == 0) scale[row] = r.scale;
-  for (int c = lane * 8; c < cols; c += 256)
-    *reinterpret_cast<uint2*>(q + row * cols + c) = bf16x8_to_s8(*reinterpret_cast<const uint4*>(xr + c), r);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) amax = max(amax, bf16x8_abs_bits(v[i]));
+  amax = warp_max_u32(amax);
+  if (T > 32) {
+    __shared__ uint32_t part[T / 32];
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < T / 32; ++w) amax = max(amax, part[w]);
+  }
+  const RowQuantS8 r = row_quant_s8(amax);
+  if (t == 0) scale[row] = r.scale;
+  uint2* qr = reinterpret_cast<uint2*>(q + row * cols);
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (t + i * T < nvec) qr[t + i * T] = bf16x8_to_s8(v[i], r);
+}
+
+// rows longer than a block's registers hold: a block per row, read twice
+__global__ void __launch_bounds__(256) quantize_long_rows_s8_kernel(const bf16* __restrict__ x, int cols,
+                                                                    uint8_t* __restrict__ q, float* __restrict__ scale) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ uint32_t part[8];
+  const size_t row = blockIdx.x;
+  const uint4* xr = reinterpret_cast<const uint4*>(x + row * cols);
+  uint2* qr = reinterpret_cast<uint2*>(q + row * cols);
+  const int nvec = cols / 8;
+  uint32_t amax = 0;
+  for (int c = threadIdx.x; c < nvec; c += 256) amax = max(amax, bf16x8_abs_bits(xr[c]));
+  amax = warp_max_u32(amax);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) amax = max(amax, part[w]);
+  const RowQuantS8 r = row_quant_s8(amax);
+  if (threadIdx.x == 0) scale[row] = r.scale;
+  for (int c = threadIdx.x; c < nvec; c += 256) qr[c] = bf16x8_to_s8(xr[c], r);
 }
 
 // ---------------------------------------------------------------------------

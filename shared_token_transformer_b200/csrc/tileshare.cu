@@ -461,29 +461,52 @@ static ts_status run_layernorm(const ts_model_desc* m, const void* x, int rows, 
   return launch_layernorm_vec<bf16, ts::ROW_T>(x, rows, d, g, b, m->eps_ln, rms, y, nullptr, nullptr, rt, st);
 }
 
-template <typename T, int Q8>
-static ts_status launch_norm_gate_vec(const void* x, const void* y, void* x_out, void* xn, uint8_t* q8, float* qs,
-                                      const ts::NormGateArgs& a, cudaStream_t st) {
-  constexpr int E = ts::Vec<T>::E;
+static constexpr int kNormGateSmem = 208 * 1024;   // dynamic shared memory of a block
+template <typename T, int NV, int Q8>
+static ts_status launch_norm_gate_nv(const void* x, const void* y, void* x_out, void* xn, uint8_t* q8, float* qs,
+                                     const ts::NormGateArgs& a, cudaStream_t st) {
+  auto kern = ts::norm_gate_kernel<T, NV, Q8>;
+  static int configured[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !configured[dev]) {
+    TS_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormGateSmem));
+    if (dev < 64) configured[dev] = 1;
+  }
+  // as many teams as a block's registers, shared memory and (several warps a team) named barriers hold, or as the rows
+  // give work to; then as many pairs of rows on their way as fit
+  const int team_warps = a.d / (32 * ts::Vec<T>::E * NV);
+  const unsigned pairs = static_cast<unsigned>((static_cast<size_t>(a.rows) + 1) / 2), sms = num_sms();
+  const size_t pair = 4 * static_cast<size_t>(a.d) * sizeof(T), vecs = 16 * static_cast<size_t>(a.d);
+  size_t teams = ts::norm_gate_threads<NV>() / (32 * team_warps);
+  teams = std::min(teams, (kNormGateSmem - vecs) / pair);
+  teams = std::min<size_t>(teams, team_warps > 1 ? 15 : ts::kNormGateTeams);
+  teams = std::min<size_t>(teams, (pairs + sms - 1) / sms);
+  const int stages = static_cast<int>(std::min<size_t>(ts::kNormGateStages, (kNormGateSmem - vecs) / (teams * pair)));
   trace_pre(st);
-#define TS_NG_CASE(NV)                                                                                         \
-  case NV: {                                                                                                   \
-    auto kern = ts::norm_gate_kernel<T, NV, Q8>;                                                               \
-    static int occ = 0;                                                                                        \
-    if (occ <= 0) {                                                                                            \
-      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, 256, 0) != cudaSuccess || occ < 1) occ = 1; \
-    }                                                                                                          \
-    const unsigned grid = std::min<unsigned>(rows_grid(a.rows), static_cast<unsigned>(occ * num_sms()));       \
-    launch_pdl(kern, dim3(grid), dim3(256), 0, st, static_cast<const T*>(x), static_cast<const T*>(y),         \
-               static_cast<T*>(x_out), static_cast<T*>(xn), q8, qs, a);                                        \
-    break;                                                                                                     \
-  }
-  switch (a.d / (32 * E)) {
-    TS_NG_CASE(1) TS_NG_CASE(2) TS_NG_CASE(3) TS_NG_CASE(4) TS_NG_CASE(5) TS_NG_CASE(6) TS_NG_CASE(7) TS_NG_CASE(8)
-    default: return fail(TS_ERR_UNSUPPORTED, "norm_gate width %d", a.d);
-  }
-#undef TS_NG_CASE
+  launch_pdl(kern, dim3(std::min<unsigned>((pairs + teams - 1) / teams, sms)), dim3(32 * team_warps * teams),
+             vecs + teams * stages * pair, st, static_cast<const T*>(x), static_cast<const T*>(y), static_cast<T*>(x_out),
+             static_cast<T*>(xn), q8, qs, a, team_warps, stages);
   return trace_post(st, "norm_gate");
+}
+
+// Few rows (at most two pairs for each block that is resident at once): a block per pair of rows.  Else vectors per
+// thread: the most, up to four, that divide the row among whole warps.
+template <typename T, int Q8>
+static ts_status launch_norm_gate(const void* x, const void* y, void* x_out, void* xn, uint8_t* q8, float* qs,
+                                  const ts::NormGateArgs& a, cudaStream_t st) {
+  const int k = a.d / (32 * ts::Vec<T>::E);
+  const long pairs = (static_cast<long>(a.rows) + 1) / 2, blocks = static_cast<long>(16 / k) * num_sms();
+  if (pairs <= 2 * blocks) {
+    trace_pre(st);
+    launch_pdl(ts::norm_gate_few_kernel<T, Q8>, dim3(static_cast<unsigned>(std::min(pairs, blocks))), dim3(32 * k), 0, st,
+               static_cast<const T*>(x), static_cast<const T*>(y), static_cast<T*>(x_out), static_cast<T*>(xn), q8, qs, a);
+    return trace_post(st, "norm_gate");
+  }
+  if (k % 4 == 0) return launch_norm_gate_nv<T, 4, Q8>(x, y, x_out, xn, q8, qs, a, st);
+  if (k % 3 == 0) return launch_norm_gate_nv<T, 3, Q8>(x, y, x_out, xn, q8, qs, a, st);
+  if (k % 2 == 0) return launch_norm_gate_nv<T, 2, Q8>(x, y, x_out, xn, q8, qs, a, st);
+  return launch_norm_gate_nv<T, 1, Q8>(x, y, x_out, xn, q8, qs, a, st);
 }
 
 // x_out = x + gate * scale * Norm_post(y); xn = Norm_pre(x_out) in the model dtype, or
@@ -509,15 +532,15 @@ static ts_status run_norm_gate(const ts_model_desc* m, const ts_norm_gate* p, co
   set_work("norm_gate", 0.0, static_cast<double>(rows) * m->d * (3.0 * e + (p->pre_g ? (q8 ? 1.0 : e) : 0.0)));
   if (m->dtype == TS_F32) {
     if (m->d % 128 == 0 && m->d <= 1024)
-      return launch_norm_gate_vec<float, ts::ROW_T>(x, y, x_out, xn, nullptr, nullptr, a, st);
+      return launch_norm_gate<float, ts::ROW_T>(x, y, x_out, xn, nullptr, nullptr, a, st);
     trace_pre(st);
     ts::norm_gate_generic_kernel<<<rows_grid(rows), 256, 0, st>>>(static_cast<const float*>(x), static_cast<const float*>(y),
                                                                  static_cast<float*>(x_out), static_cast<float*>(xn), a);
     return trace_post(st, "norm_gate_generic");
   }
-  if (q8 && m->dtype == TS_INT8) return launch_norm_gate_vec<bf16, ts::ROW_S8>(x, y, x_out, nullptr, q8, qs, a, st);
-  if (q8) return launch_norm_gate_vec<bf16, ts::ROW_E4M3>(x, y, x_out, nullptr, q8, qs, a, st);
-  return launch_norm_gate_vec<bf16, ts::ROW_T>(x, y, x_out, xn, nullptr, nullptr, a, st);
+  if (q8 && m->dtype == TS_INT8) return launch_norm_gate<bf16, ts::ROW_S8>(x, y, x_out, nullptr, q8, qs, a, st);
+  if (q8) return launch_norm_gate<bf16, ts::ROW_E4M3>(x, y, x_out, nullptr, q8, qs, a, st);
+  return launch_norm_gate<bf16, ts::ROW_T>(x, y, x_out, xn, nullptr, nullptr, a, st);
 }
 
 template <typename T, int Q8>
@@ -597,12 +620,40 @@ static ts_status run_merge(const char* name, const ts_plan_s* p, const ts_model_
   return launch_merge_vec<bf16, ts::ROW_T>(p, P, rows, d, A, nullptr, nullptr, st);
 }
 
+// Integer rows: a warp holds up to 1024 columns, a block of 128 threads up to 8192, one of
+// 256 up to 16384; longer rows are read twice.
+template <int T>
+static void launch_quantize_s8_t(const bf16* x, int rows, int cols, uint8_t* q, float* s, cudaStream_t st) {
+  constexpr int RPB = T > 128 ? 1 : 128 / T;
+  const dim3 grid((rows + RPB - 1) / RPB), block(T > 128 ? T : 128);
+  switch ((cols / 8 + T - 1) / T) {
+    case 1: launch_pdl(ts::quantize_rows_s8_kernel<T, 1>, grid, block, 0, st, x, rows, cols, q, s); break;
+    case 2: launch_pdl(ts::quantize_rows_s8_kernel<T, 2>, grid, block, 0, st, x, rows, cols, q, s); break;
+    case 3: launch_pdl(ts::quantize_rows_s8_kernel<T, 3>, grid, block, 0, st, x, rows, cols, q, s); break;
+    case 4: launch_pdl(ts::quantize_rows_s8_kernel<T, 4>, grid, block, 0, st, x, rows, cols, q, s); break;
+    default: launch_pdl(ts::quantize_rows_s8_kernel<T, 8>, grid, block, 0, st, x, rows, cols, q, s); break;
+  }
+}
+static void launch_quantize_s8(const bf16* x, int rows, int cols, uint8_t* q, float* s, cudaStream_t st) {
+  if (cols <= 1024)
+    launch_quantize_s8_t<32>(x, rows, cols, q, s, st);
+  else if (cols <= 8192)
+    launch_quantize_s8_t<128>(x, rows, cols, q, s, st);
+  else if (cols <= 16384)
+    launch_quantize_s8_t<256>(x, rows, cols, q, s, st);
+  else
+    launch_pdl(ts::quantize_long_rows_s8_kernel, dim3(rows), dim3(256), 0, st, x, cols, q, s);
+}
+
 static ts_status run_quantize(ts_dtype dt, const void* x, int rows, int cols, uint8_t* q, float* s, cudaStream_t st) {
   if (rows == 0) return TS_OK;
   set_work(dt == TS_INT8 ? "quantize_i8" : "quantize_e4m3", 0.0, static_cast<double>(rows) * cols * 3.0 + 4.0 * rows);
   trace_pre(st);
-  auto kern = dt == TS_INT8 ? ts::quantize_rows_s8_kernel : ts::quantize_rows_kernel;
-  launch_pdl(kern, dim3(rows_grid(rows)), dim3(256), 0, st, static_cast<const bf16*>(x), rows, cols, q, s);
+  if (dt == TS_INT8)
+    launch_quantize_s8(static_cast<const bf16*>(x), rows, cols, q, s, st);
+  else
+    launch_pdl(ts::quantize_rows_kernel, dim3(rows_grid(rows)), dim3(256), 0, st, static_cast<const bf16*>(x), rows, cols,
+               q, s);
   return trace_post(st, "quantize_rows");
 }
 

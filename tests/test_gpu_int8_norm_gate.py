@@ -270,7 +270,13 @@ SEAMS = [(1, 256, 4, "bf16", 1), (7, 1536, 24, "bf16", 3), (33, 512, 8, "bf16", 
          (3, 1088, 17, "f32", 2), (2500, 768, 12, "bf16", 7)]
 
 
-@pytest.mark.parametrize("rows,d,heads,dtype,groups", SEAMS)
+# rows enough for the kernel of many rows, at every number of vectors per thread and of warps per row
+MANY = [(9601, 256, 4, "bf16", 3), (4802, 512, 8, "bf16", 2), (3001, 768, 12, "bf16", 1), (2501, 1024, 16, "bf16", 4),
+        (1903, 1280, 20, "bf16", 2), (1301, 1536, 24, "bf16", 3), (1280, 1792, 28, "bf16", 2), (1251, 2048, 32, "bf16", 5),
+        (2501, 512, 8, "f32", 2), (1301, 1024, 16, "f32", 3), (1303, 896, 14, "f32", 1)]
+
+
+@pytest.mark.parametrize("rows,d,heads,dtype,groups", SEAMS + MANY)
 @pytest.mark.parametrize("block", ["ln_gelu", "rms_swiglu"])
 @pytest.mark.parametrize("mean", [0.0, 4.0])
 def test_norm_gate(rows, d, heads, dtype, groups, block, mean):
@@ -301,7 +307,7 @@ def test_norm_gate_without_a_part_and_in_place(rows, d, heads, dtype, drop):
         assert (np.abs(host(xn) - n1) <= t_n[1]).all()
 
 
-@pytest.mark.parametrize("rows,d", [(1, 256), (9, 1536), (300, 1024), (40, 2048)])
+@pytest.mark.parametrize("rows,d", [(1, 256), (9, 1536), (300, 1024), (40, 2048), (9601, 256), (1301, 1536), (2501, 1024)])
 @pytest.mark.parametrize("block", ["ln_gelu", "rms_swiglu"])
 def test_norm_gate_int8_rows(rows, d, block):
     c = Seam(rows, d, d // 64, "int8", block, 2)
@@ -320,12 +326,13 @@ def test_norm_gate_int8_rows(rows, d, block):
     assert (np.abs(host(xn)).max(1) == 127).all()
 
 
-def test_norm_gate_e4m3_rows_equal_the_quantiser():
-    """Both 8-bit forms come from the same fp32 row; e4m3 within half a step (2^-4) of the bf16 row's value."""
-    c = Seam(50, 768, 12, "fp8", "ln_gelu", 3)
-    x_out = torch.empty((50, 768), dtype=torch.bfloat16, device="cuda")
-    xn = torch.empty((50, 768), dtype=torch.uint8, device="cuda")
-    xs = torch.empty(50, device="cuda")
+@pytest.mark.parametrize("rows", [50, 3001])
+def test_norm_gate_e4m3_rows(rows):
+    """e4m3 within half a step (2^-4) of the value of the row that is normalised in 64 bits."""
+    c = Seam(rows, 768, 12, "fp8", "ln_gelu", 3)
+    x_out = torch.empty((rows, 768), dtype=torch.bfloat16, device="cuda")
+    xn = torch.empty((rows, 768), dtype=torch.uint8, device="cuda")
+    xs = torch.empty(rows, device="cuda")
     c.call(x_out, xn, xs)
     x1, n1 = c.reference()
     _, (dn, _) = c.bounds(x1)
@@ -333,31 +340,32 @@ def test_norm_gate_e4m3_rows_equal_the_quantiser():
     assert (np.abs(v - n1) <= 2.0 ** -4 * (np.abs(n1) + dn) + 2.0 ** -10 * host(xs)[:, None] + dn).all()
 
 
-def test_norm_gate_group_out_of_range_is_reported_and_leaves_the_row():
-    for dtype, d, heads in (("bf16", 512, 8), ("f32", 48, 3)):
-        c = Seam(40, d, heads, dtype, "ln_gelu", 3)
-        c.group[[7, 31]] = [3, -1]
-        x_out, xn = (torch.full((40, d), 5.0, dtype=c.dt, device="cuda") for _ in range(2))
-        c.call(x_out, xn)
-        torch.cuda.synchronize()
-        with pytest.raises(B.TileShareError) as e:
-            B.device_status()
-        assert e.value.status == 5
-        B.device_status()                                  # the word is cleared
-        c.group[[7, 31]] = 0
-        x1, n1 = c.reference()
-        t_x, (_, t_n) = c.bounds(x1)
-        keep = [r for r in range(40) if r not in (7, 31)]
-        assert (np.abs(host(x_out) - x1) <= t_x)[keep].all() and (np.abs(host(xn) - n1) <= t_n)[keep].all()
-        assert (host(x_out)[[7, 31]] == 5.0).all() and (host(xn)[[7, 31]] == 5.0).all()
+@pytest.mark.parametrize("rows,d,heads,dtype", [(40, 512, 8, "bf16"), (40, 48, 3, "f32"), (2501, 1024, 16, "bf16")])
+def test_norm_gate_group_out_of_range_is_reported_and_leaves_the_row(rows, d, heads, dtype):
+    c = Seam(rows, d, heads, dtype, "ln_gelu", 3)
+    c.group[[7, 31]] = [3, -1]
+    x_out, xn = (torch.full((rows, d), 5.0, dtype=c.dt, device="cuda") for _ in range(2))
+    c.call(x_out, xn)
+    torch.cuda.synchronize()
+    with pytest.raises(B.TileShareError) as e:
+        B.device_status()
+    assert e.value.status == 5
+    B.device_status()                                  # the word is cleared
+    c.group[[7, 31]] = 0
+    x1, n1 = c.reference()
+    t_x, (_, t_n) = c.bounds(x1)
+    keep = [r for r in range(rows) if r not in (7, 31)]
+    assert (np.abs(host(x_out) - x1) <= t_x)[keep].all() and (np.abs(host(xn) - n1) <= t_n)[keep].all()
+    assert (host(x_out)[[7, 31]] == 5.0).all() and (host(xn)[[7, 31]] == 5.0).all()
 
 
-def test_norm_gate_rows_that_are_not_finite_stay_apart():
-    c = Seam(12, 512, 8, "int8", "ln_gelu", 1)
+@pytest.mark.parametrize("rows", [12, 4901])
+def test_norm_gate_rows_that_are_not_finite_stay_apart(rows):
+    c = Seam(rows, 512, 8, "int8", "ln_gelu", 1)
     c.y[3, 5] = np.nan
     c.x[8, 100] = np.inf
-    x_out = torch.empty((12, 512), dtype=torch.bfloat16, device="cuda")
-    xn, xs = torch.empty((12, 512), dtype=torch.int8, device="cuda"), torch.empty(12, device="cuda")
+    x_out = torch.empty((rows, 512), dtype=torch.bfloat16, device="cuda")
+    xn, xs = torch.empty((rows, 512), dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
     c.call(x_out, xn, xs)
     s = host(xs)
     assert np.isnan(s[[3, 8]]).all() and np.isfinite(np.delete(s, [3, 8])).all()
