@@ -155,13 +155,24 @@ def _check(name, status):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+_current_stream = None
 
 
 def _stream(stream=None):
-    import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """The cudaStream_t of `stream`, or of torch's current stream (an address: half the time of a call of a few
+    microseconds would go into torch's stream objects)."""
+    global _current_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_stream is None:
+        import torch
+        torch.cuda.current_stream()      # initialises CUDA
+        device, raw = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        _current_stream = lambda: raw(device())   # noqa: E731
+    return _current_stream()
 
 
 # ---------------------------------------------------------------------------

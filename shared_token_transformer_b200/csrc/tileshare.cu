@@ -29,6 +29,7 @@
 #include "attention.cuh"
 #include "common.cuh"
 #include "gemm_s8.cuh"
+#include "gemm_s8_few.cuh"
 #include "gemm_tc.cuh"
 #include "plan.inl"
 #include "rowops.cuh"
@@ -815,7 +816,9 @@ static int pick_bn_s8(int M, int N, int K, bool glu) {
   struct Tile {
     int bn, rows, units, slice, epi;
   };
-  const Tile tiles[] = {{256, 256, sms / 2, 512, 2500}, {128, 128, sms, 512, 1500}, {64, 128, sms, 384, 1000}};
+  // clocks of a K slice and of a tile's epilogue, measured (2320 x 512 -> 2048 and 1000 x 6144 -> 1536): the epilogue
+  // of a tile overlaps the next tile's products, so a tile costs the longer of the two and the last epilogue comes on top
+  const Tile tiles[] = {{256, 256, sms / 2, 560, 6000}, {128, 128, sms, 540, 3300}, {64, 128, sms, 480, 2800}};
   int best = 128;
   long best_cost = -1;
   for (const Tile& t : tiles) {
@@ -829,6 +832,41 @@ static int pick_bn_s8(int M, int N, int K, bool glu) {
   }
   return best;
 }
+
+// The few-row kernel.  early: the previous kernel of the stream is the quantiser of this call, which starts only when
+// all before it has finished, so that W is complete.
+template <int NT, int U>
+static ts_status launch_gemm_s8_few(int epi, const ts::GemmFewArgs& a, cudaStream_t st) {
+  constexpr int WARPS = 8;
+  const dim3 grid((a.N + 15) / 16), block(32 * WARPS);
+  trace_pre(st);
+  switch (epi) {
+    case ts::EPI_BIAS: launch_pdl(ts::gemm_s8_few_kernel<NT, ts::EPI_BIAS, WARPS, U>, grid, block, 0, st, a); break;
+    case ts::EPI_GELU: launch_pdl(ts::gemm_s8_few_kernel<NT, ts::EPI_GELU, WARPS, U>, grid, block, 0, st, a); break;
+    case ts::EPI_RESID: launch_pdl(ts::gemm_s8_few_kernel<NT, ts::EPI_RESID, WARPS, U>, grid, block, 0, st, a); break;
+    default: launch_pdl(ts::gemm_s8_few_kernel<NT, ts::EPI_SWIGLU, WARPS, U>, grid, block, 0, st, a); break;
+  }
+  return trace_post(st, "gemm_s8_few");
+}
+static ts_status run_gemm_s8_few(int epi, const void* x, const float* x_scale, const void* W, const float* w_scale, int M,
+                                 int N, int K, const float* bias, bf16* out, bool early, cudaStream_t st) {
+  const ts::GemmFewArgs a{M, N, K, static_cast<const uint8_t*>(W), static_cast<const uint8_t*>(x), x_scale, w_scale, bias, out,
+                          K % 32 == 0 && ((reinterpret_cast<uintptr_t>(W) | reinterpret_cast<uintptr_t>(x)) & 31u) == 0, early};
+  // chunks of 128 bytes on their way per warp: three for long rows, where they save rounds (6 x 6144 -> 1536 5.9 us
+  // against 6.4 with two), two for others, whose registers leave more warps (1 x 1536 -> 6144 3.7 us against 5.2)
+  if (K > 4096) {
+    if (M <= 8) return launch_gemm_s8_few<1, 3>(epi, a, st);
+    if (M <= 16) return launch_gemm_s8_few<2, 3>(epi, a, st);
+    return launch_gemm_s8_few<4, 3>(epi, a, st);
+  }
+  if (M <= 8) return launch_gemm_s8_few<1, 2>(epi, a, st);
+  if (M <= 16) return launch_gemm_s8_few<2, 2>(epi, a, st);
+  return launch_gemm_s8_few<4, 2>(epi, a, st);
+}
+
+// Rows that the few-row kernel takes: up to 16, and up to 32 while W is at most 16 MB (32 x 6144 -> 1536 9.7 us against
+// 16.2 by tiles; 32 x 8192 -> 8192 31 us against 21, as every block reads all rows again).
+static bool few_rows(int M, double w_bytes) { return M <= 16 || (M <= 32 && w_bytes <= 16.0 * (1 << 20)); }
 
 // Y[M, N] = epi(A[M, K] W[., K]^T) of signed bytes with their scales (EPI_SWIGLU: W has 2N rows).
 static ts_status run_gemm_s8(const ts_model_desc* m, int epi, const void* A, const float* a_scale, const void* W,
@@ -876,7 +914,7 @@ static ts_status run_gemm_s8(const ts_model_desc* m, int epi, const void* A, con
 static ts_status run_gemm_tc(const char* name, const ts_model_desc* m, int epi, const void* A, const float* a_scale,
                              const void* W, const float* w_scale, int M, int N, int K, const float* bias, bf16* out,
                              const ts_layer_weights* qk, const int* pos, cudaStream_t st,
-                             const ts::RopeTable& rt = ts::RopeTable{}) {
+                             const ts::RopeTable& rt = ts::RopeTable{}, bool quantised_here = false) {
   if (M == 0) return TS_OK;
   const bool q8 = has_q8(m);
   const bool glu = epi == ts::EPI_SWIGLU;
@@ -888,6 +926,8 @@ static ts_status run_gemm_tc(const char* name, const ts_model_desc* m, int epi, 
     set_work(name, 2.0 * M * static_cast<double>(NA) * K, bytes);
   }
   TS_TRY(check_gemm_sizes(m, K, N));
+  if (m->dtype == TS_INT8 && epi != ts::EPI_QKV && few_rows(M, static_cast<double>(NA) * K))
+    return run_gemm_s8_few(epi, A, a_scale, W, w_scale, M, N, K, bias, out, quantised_here, st);
   if (m->dtype == TS_INT8) return run_gemm_s8(m, epi, A, a_scale, W, w_scale, M, N, K, bias, out, qk, pos, st, rt);
   int bn = pick_bn(M, NA);
   if (glu && bn < 128) bn = 128;    // NA = 2N is a multiple of 128
@@ -1680,7 +1720,7 @@ ts_status ts_quantize_rows_e4m3(const void* x, int rows, int cols, void* q, floa
 }
 
 ts_status ts_quantize_rows_i8(const void* x, int rows, int cols, void* q, float* scale, void* stream) {
-  if (!x || !q || !scale) return fail(TS_ERR_INVALID_ARG, "NULL argument");
+  if (rows && (!x || !q || !scale)) return fail(TS_ERR_INVALID_ARG, "NULL argument");
   if (rows < 0 || cols <= 0 || cols % 8) return fail(TS_ERR_INVALID_ARG, "need rows >= 0, cols %% 8 == 0");
   if (!aligned16(x) || !aligned16(q) || !aligned16(scale)) return fail(TS_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
   return run_quantize(TS_INT8, x, rows, cols, static_cast<uint8_t*>(q), scale, static_cast<cudaStream_t>(stream));
@@ -1722,7 +1762,8 @@ ts_status ts_op_norm_gate(const ts_model_desc* m, const ts_norm_gate* p, const v
   TS_TRY(check_model(m));
   TS_TRY(check_norm_gate(m, p));
   TS_TRY(check_row_group(row_group));
-  if (!x || !y || !x_out || rows < 0) return fail(TS_ERR_INVALID_ARG, "bad argument");
+  if ((rows && (!x || !y || !x_out)) || rows < 0) return fail(TS_ERR_INVALID_ARG, "bad argument");
+  if (rows == 0) return TS_OK;
   if ((p->pre_g != nullptr) != (xn != nullptr)) return fail(TS_ERR_INVALID_ARG, "xn goes with pre_g: both or neither");
   if (xn_scale && !xn) return fail(TS_ERR_INVALID_ARG, "xn_scale needs xn");
   if (xn_scale && !has_q8(m)) return fail(TS_ERR_INVALID_ARG, "xn_scale needs an 8-bit model (TS_FP8_E4M3 or TS_INT8)");
@@ -1745,7 +1786,8 @@ static ts_status epilogue_of(ts_epilogue epi, int* e) {
 ts_status ts_op_linear(const ts_model_desc* m, const void* x, int rows, int K, const void* W, const float* w_scale,
                        int N, const float* bias, ts_epilogue epi, void* y, void* scratch, void* stream) {
   TS_TRY(check_model(m));
-  if (!x || !W || !y || !bias || rows < 0 || K <= 0 || N <= 0) return fail(TS_ERR_INVALID_ARG, "bad argument");
+  if ((rows && (!x || !y)) || !W || !bias || rows < 0 || K <= 0 || N <= 0)
+    return fail(TS_ERR_INVALID_ARG, "bad argument");
   if (!aligned16(x) || !aligned16(W) || !aligned16(y) || !aligned16(bias)) return fail(TS_ERR_INVALID_ARG, "alignment");
   int e = 0;
   TS_TRY(epilogue_of(epi, &e));
@@ -1755,12 +1797,13 @@ ts_status ts_op_linear(const ts_model_desc* m, const void* x, int rows, int K, c
                         static_cast<float*>(y), st);
   TS_TRY(check_gemm_sizes(m, K, N));
   if (has_q8(m)) {
-    if (!scratch || !aligned16(scratch) || !w_scale || !aligned16(w_scale))
+    if ((rows && !scratch) || !aligned16(scratch) || !w_scale || !aligned16(w_scale))
       return fail(TS_ERR_INVALID_ARG, "8-bit linear needs scratch and w_scale, 16-byte aligned");
     uint8_t* q8 = static_cast<uint8_t*>(scratch);
     float* qs = reinterpret_cast<float*>(q8 + static_cast<size_t>(rows) * K);   // K % 16 == 0 keeps it aligned
     TS_TRY(run_quantize(m->dtype, x, rows, K, q8, qs, st));
-    return run_gemm_tc("linear", m, e, q8, qs, W, w_scale, rows, N, K, bias, static_cast<bf16*>(y), nullptr, nullptr, st);
+    return run_gemm_tc("linear", m, e, q8, qs, W, w_scale, rows, N, K, bias, static_cast<bf16*>(y), nullptr, nullptr, st,
+                       ts::RopeTable{}, true);
   }
   return run_gemm_tc("linear", m, e, x, nullptr, W, nullptr, rows, N, K, bias, static_cast<bf16*>(y), nullptr, nullptr, st);
 }
@@ -1769,7 +1812,7 @@ ts_status ts_op_linear_q8(const ts_model_desc* m, const void* x, const float* x_
                           const float* w_scale, int N, const float* bias, ts_epilogue epi, void* y, void* stream) {
   TS_TRY(check_model(m));
   if (!has_q8(m)) return fail(TS_ERR_INVALID_ARG, "ts_op_linear_q8 needs an 8-bit model (TS_FP8_E4M3 or TS_INT8)");
-  if (!x || !x_scale || !W || !w_scale || !y || !bias || rows < 0 || K <= 0 || N <= 0)
+  if ((rows && (!x || !x_scale || !y)) || !W || !w_scale || !bias || rows < 0 || K <= 0 || N <= 0)
     return fail(TS_ERR_INVALID_ARG, "bad argument");
   if (!aligned16(x) || !aligned16(x_scale) || !aligned16(W) || !aligned16(w_scale) || !aligned16(y) || !aligned16(bias))
     return fail(TS_ERR_INVALID_ARG, "alignment");
