@@ -10,9 +10,14 @@
 // bytes.  The sum over k may be taken in any order as long as both operands agree, so
 // the eight words of a lane's 32 bytes serve as the fragments of four products as they
 // come.  The warps' int32 sums meet in shared memory.
+//
+// With QUANT the rows arrive as bf16 (M <= 8, and K within one round of the block's
+// chunks) and every block quantises them itself (row_quant_s8) in the registers that its
+// products read: the rows are few and in L2, and the call is one launch.
 #pragma once
 
 #include "gemm_s8.cuh"
+#include "rowops.cuh"
 
 namespace ts {
 
@@ -20,12 +25,13 @@ struct GemmFewArgs {
   int M, N, K;             // N: output columns
   const uint8_t* W;        // [N, K] ([2N, K] for SwiGLU)
   const uint8_t* x;        // [M, K] signed bytes
-  const float* x_scale;    // [M]
+  const bf16* xf;          // QUANT: [M, K] bf16
+  const float* x_scale;    // [M] (not with QUANT)
   const float* w_scale;    // [N] ([2N])
   const float* bias;       // [N] ([2N])
   bf16* out;               // [M, N]; the residual for EPI_RESID
   int wide;                // K % 32 == 0, W and x 32-byte aligned
-  int early;               // W may be read before the previous kernel of the stream has finished
+  int early;               // W may be read before the previous kernel of the stream has finished (not with QUANT)
 };
 
 // The 32 bytes at p, of which `left` (a multiple of 16, or less than 1) belong to the row; zeros behind them.  wide: p
@@ -65,11 +71,25 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int NT, int EPI, int WARPS, int U>
+// 32 bf16 values of a row at p, of which `left` (a multiple of 16, or less than 1) belong to it; zeros behind them
+struct Bf32 {
+  uint4 v[4];
+};
+__device__ __forceinline__ Bf32 load_bf32(const bf16* p, int left) {
+  Bf32 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r.v[i] = left >= 16 * (i / 2 + 1) ? __ldg(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0, 0, 0, 0);
+  return r;
+}
+
+template <int NT, int EPI, bool QUANT, int WARPS, int U>
 __global__ void __launch_bounds__(32 * WARPS) gemm_s8_few_kernel(const GemmFewArgs a) {
   constexpr bool GLU = EPI == EPI_SWIGLU;
   constexpr int MG = GLU ? 2 : 1;
+  static_assert(!QUANT || NT == 1, "a block quantises at most eight rows");
   __shared__ int red[WARPS][MG][NT][4][32];
+  __shared__ uint32_t tops[QUANT ? WARPS : 1][8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, kq = (lane & 3) * 32;
   const int n0 = blockIdx.x * 16;
@@ -107,16 +127,57 @@ __global__ void __launch_bounds__(32 * WARPS) gemm_s8_few_kernel(const GemmFewAr
   }
   if (a.early) pdl_wait();
   pdl_trigger();
-#pragma unroll
-  for (int q = 0; q < NE; ++q) xs[q] = a.x_scale[min((static_cast<int>(threadIdx.x) + q * 32 * WARPS) >> 4, a.M - 1)];
+  constexpr int ROUND = WARPS * U * 128;   // bytes of K that the block's chunks cover at a time
   int acc[MG][NT][4] = {};
-  for (; k0 < a.K; k0 += WARPS * U * 128) {
+  Bf32 xb[QUANT ? U : 1];
+  RowQuantS8 rq{};
+  const bf16* xf = QUANT ? a.xf + static_cast<size_t>(min(g, a.M - 1)) * a.K + kq : nullptr;
+  if (QUANT) {
+    // largest magnitude of row g: over this lane's chunks, the four lanes of a row, the warps
+    uint32_t top = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) xb[u] = load_bf32(xf + k0 + u * 128, a.K - (k0 + u * 128 + kq));
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = max(top, bf16x8_abs_bits(xb[u].v[i]));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    if ((lane & 3) == 0) tops[warp][g] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) top = max(top, tops[w][g]);
+    rq = row_quant_s8(top);
+    const int m = threadIdx.x >> 4;        // the row of this thread's output
+    uint32_t mine = 0;
+    if (m < 8) {
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) mine = max(mine, tops[w][m]);
+    }
+#pragma unroll
+    for (int q = 0; q < NE; ++q) xs[q] = row_quant_s8(mine).scale;
+  } else {
+#pragma unroll
+    for (int q = 0; q < NE; ++q) xs[q] = a.x_scale[min((static_cast<int>(threadIdx.x) + q * 32 * WARPS) >> 4, a.M - 1)];
+  }
+  for (; k0 < a.K; k0 += ROUND) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const uint8_t* xr = a.x + static_cast<size_t>(min(nt * 8 + g, a.M - 1)) * a.K + kq;
       Bytes32 xv[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) xv[u] = load32<false>(xr + k0 + u * 128, a.K - (k0 + u * 128 + kq), a.wide);
+      for (int u = 0; u < U; ++u) {
+        if (QUANT) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint2 q = bf16x8_to_s8(xb[u].v[i], rq);
+            xv[u].w[2 * i] = q.x;
+            xv[u].w[2 * i + 1] = q.y;
+          }
+        } else {
+          xv[u] = load32<false>(xr + k0 + u * 128, a.K - (k0 + u * 128 + kq), a.wide);
+        }
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -126,7 +187,7 @@ __global__ void __launch_bounds__(32 * WARPS) gemm_s8_few_kernel(const GemmFewAr
             mma_s8(acc[i][nt], wv[u][i][0].w[p], wv[u][i][1].w[p], wv[u][i][0].w[p + 1], wv[u][i][1].w[p + 1], xv[u].w[p],
                    xv[u].w[p + 1]);
     }
-    if (k0 + WARPS * U * 128 < a.K) load_w(k0 + WARPS * U * 128);
+    if (k0 + ROUND < a.K) load_w(k0 + ROUND);
   }
 #pragma unroll
   for (int i = 0; i < MG; ++i)

@@ -835,33 +835,37 @@ static int pick_bn_s8(int M, int N, int K, bool glu) {
 
 // The few-row kernel.  early: the previous kernel of the stream is the quantiser of this call, which starts only when
 // all before it has finished, so that W is complete.
-template <int NT, int U>
+template <int NT, bool QUANT, int U>
 static ts_status launch_gemm_s8_few(int epi, const ts::GemmFewArgs& a, cudaStream_t st) {
   constexpr int WARPS = 8;
   const dim3 grid((a.N + 15) / 16), block(32 * WARPS);
   trace_pre(st);
   switch (epi) {
-    case ts::EPI_BIAS: launch_pdl(ts::gemm_s8_few_kernel<NT, ts::EPI_BIAS, WARPS, U>, grid, block, 0, st, a); break;
-    case ts::EPI_GELU: launch_pdl(ts::gemm_s8_few_kernel<NT, ts::EPI_GELU, WARPS, U>, grid, block, 0, st, a); break;
-    case ts::EPI_RESID: launch_pdl(ts::gemm_s8_few_kernel<NT, ts::EPI_RESID, WARPS, U>, grid, block, 0, st, a); break;
-    default: launch_pdl(ts::gemm_s8_few_kernel<NT, ts::EPI_SWIGLU, WARPS, U>, grid, block, 0, st, a); break;
+    case ts::EPI_BIAS: launch_pdl(ts::gemm_s8_few_kernel<NT, ts::EPI_BIAS, QUANT, WARPS, U>, grid, block, 0, st, a); break;
+    case ts::EPI_GELU: launch_pdl(ts::gemm_s8_few_kernel<NT, ts::EPI_GELU, QUANT, WARPS, U>, grid, block, 0, st, a); break;
+    case ts::EPI_RESID: launch_pdl(ts::gemm_s8_few_kernel<NT, ts::EPI_RESID, QUANT, WARPS, U>, grid, block, 0, st, a); break;
+    default: launch_pdl(ts::gemm_s8_few_kernel<NT, ts::EPI_SWIGLU, QUANT, WARPS, U>, grid, block, 0, st, a); break;
   }
   return trace_post(st, "gemm_s8_few");
 }
-static ts_status run_gemm_s8_few(int epi, const void* x, const float* x_scale, const void* W, const float* w_scale, int M,
-                                 int N, int K, const float* bias, bf16* out, bool early, cudaStream_t st) {
-  const ts::GemmFewArgs a{M, N, K, static_cast<const uint8_t*>(W), static_cast<const uint8_t*>(x), x_scale, w_scale, bias, out,
-                          K % 32 == 0 && ((reinterpret_cast<uintptr_t>(W) | reinterpret_cast<uintptr_t>(x)) & 31u) == 0, early};
+// x [M, K] signed bytes with x_scale, or xf [M, K] bf16 (M <= 8, K <= 2048).
+static ts_status run_gemm_s8_few(int epi, const void* x, const float* x_scale, const bf16* xf, const void* W,
+                                 const float* w_scale, int M, int N, int K, const float* bias, bf16* out, bool early,
+                                 cudaStream_t st) {
+  const ts::GemmFewArgs a{M, N, K, static_cast<const uint8_t*>(W), static_cast<const uint8_t*>(x), xf, x_scale, w_scale,
+                          bias, out, K % 32 == 0 && ((reinterpret_cast<uintptr_t>(W) | reinterpret_cast<uintptr_t>(x)) & 31u) == 0,
+                          early};
   // chunks of 128 bytes on their way per warp: three for long rows, where they save rounds (6 x 6144 -> 1536 5.9 us
   // against 6.4 with two), two for others, whose registers leave more warps (1 x 1536 -> 6144 3.7 us against 5.2)
+  if (xf) return launch_gemm_s8_few<1, true, 2>(epi, a, st);    // K <= 2048: one round
   if (K > 4096) {
-    if (M <= 8) return launch_gemm_s8_few<1, 3>(epi, a, st);
-    if (M <= 16) return launch_gemm_s8_few<2, 3>(epi, a, st);
-    return launch_gemm_s8_few<4, 3>(epi, a, st);
+    if (M <= 8) return launch_gemm_s8_few<1, false, 3>(epi, a, st);
+    if (M <= 16) return launch_gemm_s8_few<2, false, 3>(epi, a, st);
+    return launch_gemm_s8_few<4, false, 3>(epi, a, st);
   }
-  if (M <= 8) return launch_gemm_s8_few<1, 2>(epi, a, st);
-  if (M <= 16) return launch_gemm_s8_few<2, 2>(epi, a, st);
-  return launch_gemm_s8_few<4, 2>(epi, a, st);
+  if (M <= 8) return launch_gemm_s8_few<1, false, 2>(epi, a, st);
+  if (M <= 16) return launch_gemm_s8_few<2, false, 2>(epi, a, st);
+  return launch_gemm_s8_few<4, false, 2>(epi, a, st);
 }
 
 // Rows that the few-row kernel takes: up to 16, and up to 32 while W is at most 16 MB (32 x 6144 -> 1536 9.7 us against
@@ -909,6 +913,13 @@ static ts_status run_gemm_s8(const ts_model_desc* m, int epi, const void* A, con
   return fail(TS_ERR_INVALID_ARG, "unknown epilogue");
 }
 
+// work of a linear layer whose rows have ea bytes per element
+static void set_linear_work(const char* name, const ts_model_desc* m, int epi, int M, int N, int K, double ea) {
+  const double NA = epi == ts::EPI_SWIGLU ? 2.0 * N : N, ew = has_q8(m) ? 1.0 : 2.0;
+  set_work(name, 2.0 * M * NA * K,
+           M * static_cast<double>(K) * ea + NA * K * ew + M * static_cast<double>(N) * 2.0 * (epi == ts::EPI_RESID ? 2.0 : 1.0));
+}
+
 // Y[M, N] = A[M, K] W[N, K]^T with epilogue; A bf16 (or 8-bit + a_scale), W bf16 (or 8-bit + w_scale).
 // EPI_SWIGLU: N is the output width and W, bias, w_scale have 2N rows (gate, then up).
 static ts_status run_gemm_tc(const char* name, const ts_model_desc* m, int epi, const void* A, const float* a_scale,
@@ -919,15 +930,10 @@ static ts_status run_gemm_tc(const char* name, const ts_model_desc* m, int epi, 
   const bool q8 = has_q8(m);
   const bool glu = epi == ts::EPI_SWIGLU;
   const int NA = glu ? 2 * N : N;   // accumulator columns = rows of W
-  {
-    const double ea = q8 ? 1.0 : 2.0;
-    const double bytes = static_cast<double>(M) * K * ea + static_cast<double>(NA) * K * ea +
-                         static_cast<double>(M) * N * 2.0 * (epi == ts::EPI_RESID ? 2.0 : 1.0);
-    set_work(name, 2.0 * M * static_cast<double>(NA) * K, bytes);
-  }
+  set_linear_work(name, m, epi, M, N, K, q8 ? 1.0 : 2.0);
   TS_TRY(check_gemm_sizes(m, K, N));
   if (m->dtype == TS_INT8 && epi != ts::EPI_QKV && few_rows(M, static_cast<double>(NA) * K))
-    return run_gemm_s8_few(epi, A, a_scale, W, w_scale, M, N, K, bias, out, quantised_here, st);
+    return run_gemm_s8_few(epi, A, a_scale, nullptr, W, w_scale, M, N, K, bias, out, quantised_here, st);
   if (m->dtype == TS_INT8) return run_gemm_s8(m, epi, A, a_scale, W, w_scale, M, N, K, bias, out, qk, pos, st, rt);
   int bn = pick_bn(M, NA);
   if (glu && bn < 128) bn = 128;    // NA = 2N is a multiple of 128
@@ -1801,6 +1807,15 @@ ts_status ts_op_linear(const ts_model_desc* m, const void* x, int rows, int K, c
       return fail(TS_ERR_INVALID_ARG, "8-bit linear needs scratch and w_scale, 16-byte aligned");
     uint8_t* q8 = static_cast<uint8_t*>(scratch);
     float* qs = reinterpret_cast<float*>(q8 + static_cast<size_t>(rows) * K);   // K % 16 == 0 keeps it aligned
+    // A few rows and a W of at most 8 MB: one launch, in which the blocks quantise the rows.  1 x 1536 -> 4608 then takes
+    // 5.2 us a call from a stream against 7.4 by two launches (3.9 against 3.0 in a graph), 1 x 512 -> 2048 in a graph
+    // 2.1 against 2.6; with more of W the two win everywhere (6 x 6144 -> 1536 in a graph 6.0 against 8.8).
+    const double w_bytes = static_cast<double>(e == ts::EPI_SWIGLU ? 2 * N : N) * K;
+    if (m->dtype == TS_INT8 && rows > 0 && rows <= 8 && K <= 2048 && w_bytes <= 8.0 * (1 << 20)) {
+      set_linear_work("linear", m, e, rows, N, K, 2.0);
+      return run_gemm_s8_few(e, nullptr, nullptr, static_cast<const bf16*>(x), W, w_scale, rows, N, K, bias,
+                             static_cast<bf16*>(y), false, st);
+    }
     TS_TRY(run_quantize(m->dtype, x, rows, K, q8, qs, st));
     return run_gemm_tc("linear", m, e, q8, qs, W, w_scale, rows, N, K, bias, static_cast<bf16*>(y), nullptr, nullptr, st,
                        ts::RopeTable{}, true);
