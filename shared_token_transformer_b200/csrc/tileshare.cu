@@ -30,6 +30,7 @@
 #include "common.cuh"
 #include "gemm_s8.cuh"
 #include "gemm_s8_few.cuh"
+#include "gemm_s8_split.cuh"
 #include "gemm_tc.cuh"
 #include "plan.inl"
 #include "rowops.cuh"
@@ -219,10 +220,10 @@ static cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
-// The same launch as clusters of two CTAs (two-SM MMA pairs); grid.x is even.
+// The same launch as clusters of `size` CTAs, of which grid.x is a multiple.
 template <typename... KArgs, typename... Args>
-static cudaError_t launch_pdl_pair(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                                   Args&&... args) {
+static cudaError_t launch_pdl_cluster(int size, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                      cudaStream_t st, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -232,12 +233,19 @@ static cudaError_t launch_pdl_pair(void (*kern)(KArgs...), dim3 grid, dim3 block
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(size);
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+// Clusters of two CTAs (two-SM MMA pairs).
+template <typename... KArgs, typename... Args>
+static cudaError_t launch_pdl_pair(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                                   Args&&... args) {
+  return launch_pdl_cluster(2, kern, grid, block, smem, st, std::forward<Args>(args)...);
 }
 
 // ============================================================================
@@ -805,13 +813,65 @@ static ts_status dispatch_gemm_s8(int bn, const CUtensorMap& ta, const CUtensorM
   return launch_gemm_s8<128, STAGES, EPI, R0, R1, R2, 1>(ta, tb, td, args, st);
 }
 
-// Tile of the integer GEMM: 256 x 256 by pairs of SMs, 128 x 128 or 128 x 64 by one.
-static int pick_bn_s8(int M, int N, int K, bool glu) {
+template <int EPI>
+static ts_status launch_gemm_s8_split(const CUtensorMap& ta, const CUtensorMap& tb, const ts::GemmArgs& args, int split,
+                                      cudaStream_t st) {
+  auto kern = ts::gemm_s8_split_kernel<EPI>;
+  static int configured[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !configured[dev]) {
+    TS_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ts::SplitSmem::LAUNCH_BYTES));
+    if (dev < 64) configured[dev] = 1;
+  }
+  const int tiles = ((args.M + 127) / 128) * ((args.N + ts::kSplitBN - 1) / ts::kSplitBN);
+  trace_pre(st);
+  launch_pdl_cluster(split, kern, dim3(tiles * split), dim3(ts::kS8Threads), ts::SplitSmem::LAUNCH_BYTES, st, ta, tb, args,
+                     split);
+  return trace_post(st, "gemm_s8_split");
+}
+
+// How many clusters of `split` CTAs of the split kernel run at once on the current device: fewer than SMs / split, as a
+// cluster lies within one group of SMs.
+static int split_clusters(int split) {
+  static std::atomic<int> known[64][ts::kSplitMax + 1];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::atomic<int>* slot = dev < 64 ? &known[dev][split] : nullptr;
+  if (slot && slot->load() > 0) return slot->load() - 1;
+  auto kern = ts::gemm_s8_split_kernel<ts::EPI_BIAS>;
+  int n = 0;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ts::SplitSmem::LAUNCH_BYTES) == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(split * 64);
+    cfg.blockDim = dim3(ts::kS8Threads);
+    cfg.dynamicSmemBytes = ts::SplitSmem::LAUNCH_BYTES;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
+  }
+  if (n == 0) cudaGetLastError();
+  if (slot) slot->store(n + 1);
+  return n;
+}
+
+// Shape of the integer GEMM: tiles of 256 x 256 by pairs of SMs, of 128 x 128 or 128 x 64 by one, or (split > 1) of
+// 128 x 64 by a cluster that shares K.
+struct S8Shape {
+  int bn, split;
+};
+static S8Shape pick_s8(int M, int N, int K, int epi) {
+  const bool glu = epi == ts::EPI_SWIGLU;
   static const int forced = [] {    // tuning override, as for the other GEMMs
     const char* e = std::getenv("TS_GEMM_BN");
     return e ? std::atoi(e) : 0;
   }();
-  if (forced == 256 || forced == 128 || (forced == 64 && !glu)) return forced;
+  if (forced == 256 || forced == 128 || (forced == 64 && !glu)) return {forced, 1};
   const int sms = num_sms(), kb = (K + 127) / 128;
   struct Tile {
     int bn, rows, units, slice, epi;
@@ -819,15 +879,26 @@ static int pick_bn_s8(int M, int N, int K, bool glu) {
   // clocks of a K slice and of a tile's epilogue, measured (2320 x 512 -> 2048 and 1000 x 6144 -> 1536): the epilogue
   // of a tile overlaps the next tile's products, so a tile costs the longer of the two and the last epilogue comes on top
   const Tile tiles[] = {{256, 256, sms / 2, 560, 6000}, {128, 128, sms, 540, 3300}, {64, 128, sms, 480, 2800}};
-  int best = 128;
+  S8Shape best = {128, 1};
   long best_cost = -1;
   for (const Tile& t : tiles) {
     if (glu && t.bn == 64) continue;
     const long n = static_cast<long>((M + t.rows - 1) / t.rows) * ((N + t.bn - 1) / t.bn);
     const long cost = ((n + t.units - 1) / t.units) * std::max(kb * t.slice, t.epi) + t.epi;
     if (best_cost < 0 || cost < best_cost) {
-      best = t.bn;
+      best = {t.bn, 1};
       best_cost = cost;
+    }
+  }
+  // clusters, as long as all run at once; their exchange costs about half an epilogue more
+  if (epi != ts::EPI_QKV) {
+    const long n = static_cast<long>((M + 127) / 128) * ((N + ts::kSplitBN - 1) / ts::kSplitBN);
+    for (int split = std::min(ts::kSplitMax, kb); split > 1; --split) {
+      const long cost = (kb + split - 1) / split * 480L + 4200;
+      if (n * split <= sms && cost < best_cost && n <= split_clusters(split)) {
+        best = {ts::kSplitBN, split};
+        best_cost = cost;
+      }
     }
   }
   return best;
@@ -878,11 +949,11 @@ static ts_status run_gemm_s8(const ts_model_desc* m, int epi, const void* A, con
                              const ts_layer_weights* qk, const int* pos, cudaStream_t st, const ts::RopeTable& rt) {
   const bool glu = epi == ts::EPI_SWIGLU;
   const int NA = glu ? 2 * N : N;
-  const int bn = pick_bn_s8(M, NA, K, glu);
+  const S8Shape shape = pick_s8(M, NA, K, epi);
+  const int bn = shape.bn;
   CUtensorMap ta, tb, td;
   TS_TRY(make_tmap(&ta, A, M, K, 1, 128));
   TS_TRY(make_tmap(&tb, W, NA, K, 1, (glu || bn == 256) ? bn / 2 : bn));
-  TS_TRY(make_tmap_box(&td, out, M, N, epi == ts::EPI_QKV ? 64 : 32));   // the epilogue's boxes (s8_box)
   ts::GemmArgs g{};
   g.M = M;
   g.N = NA;
@@ -901,6 +972,13 @@ static ts_status run_gemm_s8(const ts_model_desc* m, int epi, const void* A, con
     g.rope_cs = rt.cs;
     for (int a = 0; a < 3; ++a) g.rope_off[a] = rt.off[a];
   }
+  if (shape.split > 1) switch (epi) {
+      case ts::EPI_BIAS: return launch_gemm_s8_split<ts::EPI_BIAS>(ta, tb, g, shape.split, st);
+      case ts::EPI_GELU: return launch_gemm_s8_split<ts::EPI_GELU>(ta, tb, g, shape.split, st);
+      case ts::EPI_RESID: return launch_gemm_s8_split<ts::EPI_RESID>(ta, tb, g, shape.split, st);
+      default: return launch_gemm_s8_split<ts::EPI_SWIGLU>(ta, tb, g, shape.split, st);
+    }
+  TS_TRY(make_tmap_box(&td, out, M, N, epi == ts::EPI_QKV ? 64 : 32));   // the epilogue's boxes (s8_box)
   switch (epi) {
     case ts::EPI_BIAS: return dispatch_gemm_s8<ts::EPI_BIAS, 0, 32, 32>(bn, ta, tb, td, g, st);
     case ts::EPI_GELU: return dispatch_gemm_s8<ts::EPI_GELU, 0, 32, 32>(bn, ta, tb, td, g, st);
