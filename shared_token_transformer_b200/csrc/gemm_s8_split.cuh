@@ -7,9 +7,9 @@
 // tile's four parts of sixteen accumulator columns is finished by one CTA of the
 // cluster.  Bound by the slices' latency through the ring: with S stretches the chain
 // is S times shorter: 257 x 4096 -> 1024 (48 tiles, S = 2) takes 8.5 us instead of 12.0,
-128 x 4096 -> 1024 (16 tiles, S = 6) 6.3 instead of 11.7.  Only as many clusters as run
-at once are used; a second wave would cost more than splitting saves (S = 3 took 14.1 us
-on the first of these).
+// 128 x 4096 -> 1024 (16 tiles, S = 6) 6.3 instead of 11.7.  Only as many clusters as run
+// at once are used; a second wave would cost more than splitting saves (S = 3 took 14.1 us
+// on the first of these).
 #pragma once
 
 #include "gemm_s8.cuh"
