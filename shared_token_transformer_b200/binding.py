@@ -158,21 +158,31 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-_current_stream = None
+_device = _raw_stream = None      # torch's current device number, and the stream of a device as an address
+
+
+def _cuda():
+    global _device, _raw_stream
+    import torch
+    torch.cuda.init()
+    _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    return _device
 
 
 def _stream(stream=None):
-    """The cudaStream_t of `stream`, or of torch's current stream (an address: half the time of a call of a few
-    microseconds would go into torch's stream objects)."""
-    global _current_stream
+    """The cudaStream_t of `stream`, or of torch's current stream (as an address: torch's stream objects would take half
+    the time of a call of a few microseconds)."""
     if stream is not None:
         return stream.cuda_stream
-    if _current_stream is None:
-        import torch
-        torch.cuda.current_stream()      # initialises CUDA
-        device, raw = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-        _current_stream = lambda: raw(device())   # noqa: E731
-    return _current_stream()
+    if _raw_stream is None:
+        _cuda()
+    return _raw_stream(_device())
+
+
+def _unfit(fn):
+    """The 8-bit and seam calls take row-major tensors of the current device whose sizes belong together; others are
+    refused here, since a pointer does not tell."""
+    raise TileShareError(fn, 1, "a tensor is not contiguous, not on the current device, or too small for the call")
 
 
 # ---------------------------------------------------------------------------
@@ -237,13 +247,22 @@ def layer_weights(tensors):
 
 
 def _keep(struct, tensors):
+    """Fill a struct of fp32 vectors [d], gates [groups, d] and an int32 row_group, and keep the tensors alive."""
+    width, groups = set(), set()
     for n, t in tensors.items():
-        if t is not None:
-            setattr(struct, n, t.data_ptr())
-    gates = [t for n, t in tensors.items() if n.startswith("gate") and t is not None]
-    if len({t.shape[0] for t in gates}) > 1:
-        raise ValueError("the gates have different numbers of groups")
-    struct.groups = gates[0].shape[0] if gates else 0
+        if t is None:
+            continue
+        if not t.is_contiguous() or t.itemsize != 4:
+            raise ValueError(f"{n} must be contiguous with elements of 32 bits")
+        setattr(struct, n, t.data_ptr())
+        if n.startswith("gate"):
+            groups.add(t.shape[0])
+        if n != "row_group":
+            width.add(t.shape[-1])
+    if len(groups) > 1 or len(width) > 1:
+        raise ValueError("the vectors have different widths or the gates different numbers of groups")
+    struct.groups = groups.pop() if groups else 0
+    struct.width = width.pop() if width else 0
     struct._tensors = dict(tensors)
     return struct
 
@@ -288,7 +307,15 @@ def block_partial(plan, model, weights, shared_ops, X, ws, stream=None):
                                                       ws.numel() * ws.element_size(), _stream(stream)))
 
 
+def _sandwich_rows(fn, model, sandwich, rows):
+    group = sandwich._tensors.get("row_group")
+    if sandwich.width not in (model.d, 0) or (group is not None and group.numel() != rows):
+        raise TileShareError(fn, 1, f"sandwich vectors of width {sandwich.width} or a row_group that is not of {rows} rows")
+
+
 def block_shared_sandwich(plan, model, weights, sandwich, S, ws, stream=None):
+    """ts_block_shared_sandwich: block_shared with norms, gates and scales (sandwich_weights) around its halves."""
+    _sandwich_rows("ts_block_shared_sandwich", model, sandwich, plan.U + plan.T * plan.R)
     _check("ts_block_shared_sandwich",
            lib().ts_block_shared_sandwich(plan.handle, ctypes.byref(model), ctypes.byref(weights),
                                           ctypes.byref(sandwich), _ptr(S), _ptr(ws),
@@ -296,6 +323,8 @@ def block_shared_sandwich(plan, model, weights, sandwich, S, ws, stream=None):
 
 
 def block_tiled_sandwich(plan, model, weights, sandwich, X, ws, stream=None):
+    """ts_block_tiled_sandwich: the same around block_tiled."""
+    _sandwich_rows("ts_block_tiled_sandwich", model, sandwich, plan.T * plan.N)
     _check("ts_block_tiled_sandwich",
            lib().ts_block_tiled_sandwich(plan.handle, ctypes.byref(model), ctypes.byref(weights),
                                          ctypes.byref(sandwich), _ptr(X), _ptr(ws),
@@ -347,6 +376,10 @@ def quantize_rows_e4m3(x, q, scale, stream=None):
 
 def quantize_rows_i8(x, q, scale, stream=None):
     rows, cols = x.shape
+    if not (x.is_contiguous() and q.is_contiguous() and x.nbytes == 2 * rows * cols <= 2 * q.nbytes and
+            q.itemsize == 1 and scale.nbytes >= 4 * rows and
+            x.get_device() == q.get_device() == scale.get_device() == (_device or _cuda())()):
+        _unfit("ts_quantize_rows_i8")
     _check("ts_quantize_rows_i8", lib().ts_quantize_rows_i8(_ptr(x), rows, cols, _ptr(q), _ptr(scale),
                                                             _stream(stream)))
 
@@ -366,25 +399,57 @@ def op_layernorm(model, x, g, b, y, stream=None):
 
 
 def op_norm_gate(model, gates, x, y, x_out, xn=None, xn_scale=None, row_group=None, stream=None):
-    """ts_op_norm_gate: x_out = x + gate * scale * Norm_post(y), xn = Norm_pre(x_out); with xn_scale, xn is 8-bit rows."""
-    _check("ts_op_norm_gate", lib().ts_op_norm_gate(ctypes.byref(model), ctypes.byref(gates), _ptr(x), _ptr(y),
-                                                    _ptr(row_group), x.shape[0], _ptr(x_out), _ptr(xn),
-                                                    _ptr(xn_scale), _stream(stream)))
+    """ts_op_norm_gate: x_out = x + gate * scale * Norm_post(y) and xn = Norm_pre(x_out), as 8-bit rows with xn_scale."""
+    rows, d = x.shape
+    e = 4 if model.dtype == TS_F32 else 2
+    if not (d == model.d and gates.width in (d, 0) and x.nbytes == y.nbytes == rows * d * e <= x_out.nbytes and
+            x_out.itemsize == e and x.is_contiguous() and y.is_contiguous() and x_out.is_contiguous() and
+            x.get_device() == x_out.get_device() == (_device or _cuda())()):
+        _unfit("ts_op_norm_gate")
+    if xn is not None and not (xn.is_contiguous() and xn.itemsize == (e if xn_scale is None else 1) and
+                               xn.nbytes >= rows * d * xn.itemsize and
+                               (xn_scale is None or xn_scale.nbytes >= 4 * rows)):
+        _unfit("ts_op_norm_gate")
+    if row_group is not None and row_group.nbytes != 4 * rows:
+        _unfit("ts_op_norm_gate")
+    status = (_lib or lib()).ts_op_norm_gate(ctypes.byref(model), ctypes.byref(gates), x.data_ptr(), y.data_ptr(),
+                                             _ptr(row_group), rows, x_out.data_ptr(), _ptr(xn), _ptr(xn_scale),
+                                             _stream(stream))
+    if status:
+        _check("ts_op_norm_gate", status)
 
 
 def op_linear(model, x, W, bias, y, epi=TS_EPI_BIAS, w_scale=None, scratch=None, stream=None):
     rows, K = x.shape
-    N = W.shape[0] // 2 if epi == TS_EPI_BIAS_SWIGLU else W.shape[0]     # output width
-    _check("ts_op_linear", lib().ts_op_linear(ctypes.byref(model), _ptr(x), rows, K, _ptr(W), _ptr(w_scale), N,
-                                              _ptr(bias), epi, _ptr(y), _ptr(scratch), _stream(stream)))
+    wide = W.shape[0]
+    N = wide // 2 if epi == TS_EPI_BIAS_SWIGLU else wide     # output width
+    if model.dtype == TS_INT8 and not (
+            x.nbytes == 2 * rows * K and W.nbytes == wide * K and y.nbytes >= 2 * rows * N and y.itemsize == 2 and
+            w_scale is not None and scratch is not None and bias.nbytes >= 4 * wide <= w_scale.nbytes and
+            scratch.nbytes >= rows * (K + 4) and x.is_contiguous() and W.is_contiguous() and y.is_contiguous() and
+            x.get_device() == y.get_device() == (_device or _cuda())()):
+        _unfit("ts_op_linear")
+    status = (_lib or lib()).ts_op_linear(ctypes.byref(model), x.data_ptr(), rows, K, W.data_ptr(), _ptr(w_scale), N,
+                                          _ptr(bias), epi, y.data_ptr(), _ptr(scratch), _stream(stream))
+    if status:
+        _check("ts_op_linear", status)
 
 
 def op_linear_q8(model, x, x_scale, W, w_scale, bias, y, epi=TS_EPI_BIAS, stream=None):
     """ts_op_linear_q8: the linear layer of rows that are 8-bit already, with their scales."""
     rows, K = x.shape
-    N = W.shape[0] // 2 if epi == TS_EPI_BIAS_SWIGLU else W.shape[0]     # output width
-    _check("ts_op_linear_q8", lib().ts_op_linear_q8(ctypes.byref(model), _ptr(x), _ptr(x_scale), rows, K, _ptr(W),
-                                                    _ptr(w_scale), N, _ptr(bias), epi, _ptr(y), _stream(stream)))
+    wide = W.shape[0]
+    N = wide // 2 if epi == TS_EPI_BIAS_SWIGLU else wide     # output width
+    if not (x.nbytes == rows * K and W.nbytes == wide * K and y.nbytes >= 2 * rows * N and y.itemsize == 2 and
+            bias.nbytes >= 4 * wide <= w_scale.nbytes and x_scale.nbytes >= 4 * rows and x.is_contiguous() and
+            W.is_contiguous() and y.is_contiguous() and
+            x.get_device() == y.get_device() == (_device or _cuda())()):
+        _unfit("ts_op_linear_q8")
+    status = (_lib or lib()).ts_op_linear_q8(ctypes.byref(model), x.data_ptr(), x_scale.data_ptr(), rows, K,
+                                             W.data_ptr(), w_scale.data_ptr(), N, bias.data_ptr(), epi, y.data_ptr(),
+                                             _stream(stream))
+    if status:
+        _check("ts_op_linear_q8", status)
 
 
 def op_qkv(plan, model, weights, mode, state, qkv, scratch, stream=None):

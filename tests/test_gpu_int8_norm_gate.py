@@ -572,6 +572,63 @@ def test_sandwich_layers(dtype, block, parts):
         t = dev(state.reshape(-1, cfg.d), c.dt)
         fn, ref = ((B.block_tiled_sandwich, OL.block_tiled_sandwich) if tiled else
                    (B.block_shared_sandwich, OL.block_shared_sandwich))
+        with pytest.raises(B.TileShareError):
+            fn(c.plan, c.m, c.w[0], B.sandwich_weights(row_group=sw._tensors["row_group"][1:]), t, c.ws())
+        with pytest.raises(B.TileShareError):
+            fn(c.plan, c.m, c.w[0], B.sandwich_weights(scale1=torch.ones(2 * cfg.d, device="cuda")), t, c.ws())
         fn(c.plan, c.m, c.w[0], sw, t, c.ws())
         want = ref(state, c.p[0], dict(vec, row_group=group), c.om, c.op).reshape(-1, cfg.d)
         assert rel_l2(host(t), want) < TOL[dtype]
+
+
+# ---------------------------------------------------------------------------
+# refusals that need device tensors
+# ---------------------------------------------------------------------------
+def test_binding_refuses_tensors_that_do_not_fit():
+    M, K, N = 8, 128, 64
+    x = torch.zeros((M, K), dtype=torch.int8, device="cuda")
+    w = torch.zeros((N, K), dtype=torch.int8, device="cuda")
+    s, b = torch.ones(N, device="cuda"), torch.zeros(N, device="cuda")
+    y = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+    xb = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    scratch = torch.zeros(M * (K + 4), dtype=torch.uint8, device="cuda")
+    ok = dict(model=model(), x=x, x_scale=s, W=w, w_scale=s, bias=b, y=y)
+    B.op_linear_q8(**ok)
+    wide = torch.zeros((M, 2 * K), dtype=torch.int8, device="cuda")
+    for bad in ({"x": wide[:, :K]}, {"x": x[::2].t().contiguous()[:, :4]}, {"W": w.t()}, {"W": w[:, :64]}, {"x": x.cpu()},
+                {"x": xb}, {"y": y.float()}, {"y": y[: M - 1]}, {"bias": b[: N - 1]}, {"w_scale": s[:8]},
+                {"x_scale": s[: M - 1]}, {"W": w.bfloat16()}, {"y": y.t()}):
+        with pytest.raises(B.TileShareError) as e:
+            B.op_linear_q8(**dict(ok, **bad))
+        assert e.value.status == 1
+    lin = dict(model=model(), x=xb, W=w, bias=b, y=y, w_scale=s, scratch=scratch)
+    B.op_linear(**lin)
+    for bad in ({"x": x}, {"scratch": scratch[:-1]}, {"scratch": None}, {"w_scale": None}, {"W": w[:, ::2]}, {"x": xb[:, ::2]}):
+        with pytest.raises(B.TileShareError) as e:
+            B.op_linear(**dict(lin, **bad))
+        assert e.value.status == 1
+    c = Seam(M, 256, 4, "bf16", "ln_gelu", 1)
+    x1 = torch.empty((M, 256), dtype=torch.bfloat16, device="cuda")
+    for out in (x1.t(), x1[:-1], x1.float(), x1.cpu(), x1.to(torch.int8)):
+        with pytest.raises(B.TileShareError):
+            c.call(out, x1)
+    with pytest.raises(B.TileShareError):
+        c.call(x1, x1.to(torch.int8))                      # 8-bit rows need their scales
+    with pytest.raises(B.TileShareError):                  # vectors of another width
+        B.op_norm_gate(c.m, B.norm_gate_desc(scale=torch.ones(128, device="cuda")), x1, x1, x1)
+    q = torch.empty((M, K), dtype=torch.int8, device="cuda")
+    for args in ((xb, q[:-1], s), (xb.t(), q, s), (xb.float(), q, s), (xb, q, s[:4])):
+        with pytest.raises(B.TileShareError):
+            B.quantize_rows_i8(*args)
+
+
+def test_calls_with_no_rows_do_nothing():
+    w, s = torch.zeros((64, 128), dtype=torch.int8, device="cuda"), torch.ones(64, device="cuda")
+    none = lambda d, t: torch.empty((0, d), dtype=t, device="cuda")   # noqa: E731
+    n = B.launch_count()
+    B.op_linear_q8(model(), none(128, torch.int8), s[:0], w, s, s, none(64, torch.bfloat16))
+    B.op_linear(model(), none(128, torch.bfloat16), w, s, none(64, torch.bfloat16), w_scale=s, scratch=s)
+    B.quantize_rows_i8(none(128, torch.bfloat16), none(128, torch.int8), s[:0])
+    x = none(256, torch.bfloat16)
+    B.op_norm_gate(model(), B.norm_gate_desc(), x, x, x)
+    assert B.launch_count() == n

@@ -165,3 +165,11 @@ def test_gates_of_different_groups_are_refused():
     import torch
     with pytest.raises(ValueError):
         B.sandwich_weights(gate1=torch.zeros(2, 64), gate2=torch.zeros(3, 64))
+    with pytest.raises(ValueError):
+        B.norm_gate_desc(post_g=torch.zeros(64), scale=torch.zeros(32))
+    with pytest.raises(ValueError):
+        B.norm_gate_desc(post_g=torch.zeros(64, dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        B.norm_gate_desc(gate=torch.zeros(64, 2).t())
+    g = B.norm_gate_desc(gate=torch.zeros(2, 64), scale=torch.zeros(64))
+    assert (g.groups, g.width) == (2, 64)
