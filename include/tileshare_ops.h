@@ -66,7 +66,9 @@ ts_status ts_op_norm_gate(const ts_model_desc* model, const ts_norm_gate* p, con
    out-projection and MLP once per token).  x [rows, K], W [N, K], y [rows, N], in
    the model dtype (8-bit dtypes: x and y bf16, W 8-bit with per-row scales w_scale [N];
    x is quantised per row inside the call using `scratch`, which must hold
-   rows * K + 4 * rows bytes; scratch is unused otherwise and may be NULL).
+   rows * K + 4 * rows bytes and belongs to the call until it has run: calls in flight
+   at once, captured graphs among them, need one each; scratch is unused otherwise and
+   may be NULL).
    bf16/e4m3 need K % 64 == 0 and N % 64 == 0 (K % 128 for e4m3); int8 needs
    K % 16 == 0, N % 8 == 0 and K <= 131056. */
 ts_status ts_op_linear(const ts_model_desc* model, const void* x, int rows, int K,

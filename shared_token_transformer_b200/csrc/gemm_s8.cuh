@@ -76,6 +76,11 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max_nan(float a, float b) {   // the larger, NaN if either is
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 // GELU of a pair:
 //   x (1 + erf(x / sqrt 2)) / 2 = max(x, 0) - a 2^Q(a),   a = |x|,   2^Q(a) = erfc(a / sqrt 2) / 2
 // with Q a polynomial of degree 6 fitted here over [0, 8] (Lawson's iteration, each error weighted by what it does to
@@ -85,7 +90,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
 __device__ __forceinline__ uint64_t gelu_exp2(uint64_t x2) {
   const float x0 = lo_f32(x2), x1 = hi_f32(x2);
   const uint64_t na = pack_f32x2(fmaxf(-fabsf(x0), -8.f), fmaxf(-fabsf(x1), -8.f));
-  const uint64_t relu = pack_f32x2(fmaxf(x0, 0.f), fmaxf(x1, 0.f));
+  const uint64_t relu = pack_f32x2(max_nan(x0, 0.f), max_nan(x1, 0.f));    // carries a NaN into the result
   uint64_t q = fma_f32x2(splat_f32x2(2.9704213375225663e-05f), na, splat_f32x2(0.0007424539653584361f));
   q = fma_f32x2(q, na, splat_f32x2(0.008002202026546001f));
   q = fma_f32x2(q, na, splat_f32x2(0.05330503359436989f));
@@ -220,6 +225,13 @@ __global__ void __launch_bounds__(kS8Threads, 1)
           bulk_load(dst + 6 * BN, args.bias + n_out + c0, bytes, vbar);
         }
       }
+      // no copy may still be landing when the CTA exits (matters only after a timeout; of a pair the even CTA waits for
+      // both, and the odd one leaves after it)
+      if (!ok) {
+        if (leader)
+          for (uint32_t n = it > STAGES ? it - STAGES : 0; n < it; ++n) mbar_wait(bar_full + 8 * (n % STAGES), (n / STAGES) & 1);
+        for (uint32_t n = j > 2 ? j - 2 : 0; n < j; ++n) mbar_wait(bar_vfull + 8 * (n & 1), (n >> 1) & 1);
+      }
     }
   } else if (warp == kS8MmaWarp) {
     if (lane == 0 && leader) {
@@ -267,7 +279,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
     uint8_t* srow = smem + SM::EPI_OFFSET + warp * SM::BOX_BYTES + lane * (CW * 2);
     const int sx = CW == 64 ? (lane & 7) : ((lane >> 1) & 3);
     auto piece = [&](int q) { return reinterpret_cast<uint4*>(srow + ((q ^ sx) << 4)); };
-    uint32_t nres = 0, j = 0;
+    uint32_t nload = 0, nres = 0, j = 0;   // residual boxes asked for and waited for
     const int n_out = GLU ? args.N / 2 : args.N;
     const uint32_t tempty = CG == 2 ? cluster_map(bar_tempty, 0) : bar_tempty;
     auto release = [&](uint32_t acc) {      // this warp's last TMEM read of the tile is done
@@ -299,6 +311,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
           mbar_expect_tx(rbar, SM::BOX_BYTES);
           tma_load_2d(stg, &tmD, rbar, c, row0);
         }
+        ++nload;
       };
       if (EPI == EPI_RESID && mine) load_residual(col);
       bool ok = mbar_wait(bar_vfull + 8 * acc, use & 1) && mbar_wait(bar_tfull + 8 * acc, use & 1);
@@ -404,7 +417,10 @@ __global__ void __launch_bounds__(kS8Threads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_vempty + 8 * acc);
     }
-    if (lane == 0) bulk_wait_all();
+    if (lane == 0) {
+      if (EPI == EPI_RESID && nload != nres) mbar_wait(rbar, nres & 1);   // after a timeout: the load in flight
+      bulk_wait_all();
+    }
   }
   tc_fence_before();
   __syncthreads();

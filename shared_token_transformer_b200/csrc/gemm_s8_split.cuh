@@ -107,9 +107,11 @@ __global__ void __launch_bounds__(kS8Threads, 1)
   float acc[16], ws[16], bi[16], rs = 0.f;
   if (warp == kS8TmaWarp) {
     if (lane == 0) {
-      for (int kb = kb0; kb < kb1; ++kb) {
-        const uint32_t it = kb - kb0, s = it % STAGES;
-        if (it >= STAGES && !mbar_wait(bar_empty + 8 * s, ((it / STAGES) - 1) & 1)) break;
+      uint32_t it = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const uint32_t s = it % STAGES;
+        if (it >= STAGES && !mbar_wait(bar_empty + 8 * s, ((it / STAGES) - 1) & 1)) { ok = false; break; }
         const uint32_t sa = sbase + s * SM::STAGE_BYTES;
         mbar_expect_tx(bar_full + 8 * s, SM::STAGE_BYTES);
         tma_load_2d(sa, &tmA, bar_full + 8 * s, kb * KE, m0);
@@ -120,6 +122,8 @@ __global__ void __launch_bounds__(kS8Threads, 1)
           tma_load_2d(sa + SM::A_BYTES, &tmB, bar_full + 8 * s, kb * KE, n0);
         }
       }
+      // no copy may still be landing when the CTA exits (matters only after a timeout)
+      for (uint32_t n = ok ? it : it > STAGES ? it - STAGES : 0; n < it; ++n) mbar_wait(bar_full + 8 * (n % STAGES), (n / STAGES) & 1);
     }
     __syncwarp();
   } else if (warp == kS8MmaWarp) {

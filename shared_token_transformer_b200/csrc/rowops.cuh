@@ -281,7 +281,9 @@ __global__ void __launch_bounds__(256) norm_gate_few_kernel(const T* x, const T*
                                                             float* qscale, const NormGateArgs a) {
   __shared__ __align__(16) float red[2][2][8];
   constexpr int E = Vec<T>::E, P = E / 2;
+  constexpr bool RAGGED = sizeof(T) == 4;    // fp32 rows may end inside a warp: threads behind the end hold zeros
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = threadIdx.x * E;
+  const bool in = !RAGGED || c0 < a.d;
   const float inv_d = 1.0f / static_cast<float>(a.d);
   if (threadIdx.x < 32) (&red[0][0][0])[threadIdx.x] = 0.f;    // warps that a block lacks add nothing
   __syncthreads();
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(256) norm_gate_few_kernel(const T* x, const T*
   auto pairs_of = [&](const float* v, float fill, uint64_t (&p)[P]) {   // this thread's columns of a vector
 #pragma unroll
     for (int i = 0; i < P; i += 2) {
-      const float4 f = v ? __ldg(reinterpret_cast<const float4*>(v + c0 + 2 * i)) : make_float4(fill, fill, fill, fill);
+      const float4 f = v && in ? __ldg(reinterpret_cast<const float4*>(v + c0 + 2 * i)) : make_float4(fill, fill, fill, fill);
       p[i] = pack_f32x2(f.x, f.y);
       p[i + 1] = pack_f32x2(f.z, f.w);
     }
@@ -349,8 +351,8 @@ __global__ void __launch_bounds__(256) norm_gate_few_kernel(const T* x, const T*
       sum2(s0, s1);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        v0[i] = add_f32x2(v0[i], splat_f32x2(-s0 * inv_d));
-        v1[i] = add_f32x2(v1[i], splat_f32x2(-s1 * inv_d));
+        v0[i] = in ? add_f32x2(v0[i], splat_f32x2(-s0 * inv_d)) : 0ull;
+        v1[i] = in ? add_f32x2(v1[i], splat_f32x2(-s1 * inv_d)) : 0ull;
       }
     }
     uint64_t t0 = 0ull, t1 = 0ull;
@@ -373,10 +375,11 @@ __global__ void __launch_bounds__(256) norm_gate_few_kernel(const T* x, const T*
     const bool two = row + 1 < rows;
     const size_t o0 = row * a.d + c0, o1 = two ? o0 + a.d : o0;
     uint64_t x0[P], x1[P], v0[P], v1[P];
-    unpack_pairs<T>(*reinterpret_cast<const uint4*>(y + o0), v0);
-    unpack_pairs<T>(*reinterpret_cast<const uint4*>(y + o1), v1);
-    unpack_pairs<T>(*reinterpret_cast<const uint4*>(x + o0), x0);
-    unpack_pairs<T>(*reinterpret_cast<const uint4*>(x + o1), x1);
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    unpack_pairs<T>(in ? *reinterpret_cast<const uint4*>(y + o0) : zero, v0);
+    unpack_pairs<T>(in ? *reinterpret_cast<const uint4*>(y + o1) : zero, v1);
+    unpack_pairs<T>(in ? *reinterpret_cast<const uint4*>(x + o0) : zero, x0);
+    unpack_pairs<T>(in ? *reinterpret_cast<const uint4*>(x + o1) : zero, x1);
     const int g0 = norm_gate_group(a, row), g1 = two ? norm_gate_group(a, row + 1) : -1;
     if (g0 >= 0 && g0 != gs_group) load_gate(g0);
     if (a.post_g) norm2(v0, v1, post_g, post_b);
@@ -385,13 +388,17 @@ __global__ void __launch_bounds__(256) norm_gate_few_kernel(const T* x, const T*
     if (g1 >= 0 && g1 != gs_group) load_gate(g1);
 #pragma unroll
     for (int i = 0; i < P; ++i) v1[i] = fma_f32x2(gs[i], v1[i], x1[i]);
-    if (g0 >= 0) *reinterpret_cast<uint4*>(x_out + o0) = pack_pairs(v0);
-    if (g1 >= 0) *reinterpret_cast<uint4*>(x_out + o1) = pack_pairs(v1);
+    if (g0 >= 0 && in) *reinterpret_cast<uint4*>(x_out + o0) = pack_pairs(v0);
+    if (g1 >= 0 && in) *reinterpret_cast<uint4*>(x_out + o1) = pack_pairs(v1);
     if (!a.pre_g) continue;
+    if (!in) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) v0[i] = v1[i] = 0ull;
+    }
     norm2(v0, v1, pre_g, pre_b);
     if (Q8 == ROW_T) {
-      if (g0 >= 0) *reinterpret_cast<uint4*>(xn + o0) = pack_pairs(v0);
-      if (g1 >= 0) *reinterpret_cast<uint4*>(xn + o1) = pack_pairs(v1);
+      if (g0 >= 0 && in) *reinterpret_cast<uint4*>(xn + o0) = pack_pairs(v0);
+      if (g1 >= 0 && in) *reinterpret_cast<uint4*>(xn + o1) = pack_pairs(v1);
     } else {
       uint32_t m0 = 0, m1 = 0;
 #pragma unroll
@@ -430,11 +437,14 @@ __global__ void __launch_bounds__(norm_gate_threads<NV>(), 1)
   __shared__ __align__(16) float red[kNormGateTeams][2][2][kNormGateTeamWarps];
   __shared__ __align__(8) uint64_t bars[kNormGateTeams][kNormGateStages][2];    // y, x
   constexpr int E = Vec<T>::E, P = E / 2, Q = E / 4;
+  constexpr bool RAGGED = sizeof(T) == 4;    // fp32 rows may end inside a team's vectors: what lies behind is zero
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % team_warps, team = (threadIdx.x >> 5) / team_warps;
   const int tsize = 32 * team_warps, t = threadIdx.x - team * tsize, teams = blockDim.x / tsize;
   const uint32_t rowbytes = static_cast<uint32_t>(a.d) * sizeof(T);
   const float inv_d = 1.0f / static_cast<float>(a.d);
-  uint8_t* ring = smem + static_cast<size_t>(16) * a.d + static_cast<size_t>(team) * stages * 4 * rowbytes;
+  const int quads = RAGGED ? NV * Q * tsize : a.d / 4;    // four-column quads of a vector in shared memory
+  auto in = [&](int i) -> bool { return !RAGGED || (i * tsize + t) * E < a.d; };
+  uint8_t* ring = smem + static_cast<size_t>(64) * quads + static_cast<size_t>(team) * stages * 4 * rowbytes;
   if (t == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(smem_u32(&bars[team][s][0]), 1);
@@ -475,14 +485,13 @@ __global__ void __launch_bounds__(norm_gate_threads<NV>(), 1)
   // float4s apart, so that a warp reads them without bank conflicts.
   const float* src[4] = {a.post_g, a.rms ? nullptr : a.post_b, a.pre_g, a.rms ? nullptr : a.pre_b};
   float4* vecs = reinterpret_cast<float4*>(smem);
-  const int quads = a.d / 4;
   for (int m0 = team; m0 < 4 * NV * Q; m0 += 8 * teams) {      // the teams take turns, eight loads in flight
     float4 f[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int m = m0 + u * teams, k = m / (NV * Q), c = m % (NV * Q);
       const float* v = k == 0 ? src[0] : k == 1 ? src[1] : k == 2 ? src[2] : src[3];
-      f[u] = m < 4 * NV * Q && v ? __ldg(reinterpret_cast<const float4*>(v) + (c / Q * tsize + t) * Q + c % Q)
+      f[u] = m < 4 * NV * Q && v && in(c / Q) ? __ldg(reinterpret_cast<const float4*>(v) + (c / Q * tsize + t) * Q + c % Q)
                                  : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
@@ -500,8 +509,8 @@ __global__ void __launch_bounds__(norm_gate_threads<NV>(), 1)
       for (int j = 0; j < Q; ++j) {
         const size_t c = static_cast<size_t>(i * tsize + t) * E + 4 * j;
         float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
-        if (a.gate) f = __ldg(reinterpret_cast<const float4*>(a.gate + static_cast<size_t>(group) * a.d + c));
-        if (a.scale) {
+        if (a.gate && in(i)) f = __ldg(reinterpret_cast<const float4*>(a.gate + static_cast<size_t>(group) * a.d + c));
+        if (a.scale && in(i)) {
           const float4 sc = __ldg(reinterpret_cast<const float4*>(a.scale + c));
           f.x *= sc.x; f.y *= sc.y; f.z *= sc.z; f.w *= sc.w;
         }
@@ -583,8 +592,8 @@ __global__ void __launch_bounds__(norm_gate_threads<NV>(), 1)
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-          v0[i][p] = add_f32x2(v0[i][p], m0);
-          v1[i][p] = add_f32x2(v1[i][p], m1);
+          v0[i][p] = in(i) ? add_f32x2(v0[i][p], m0) : 0ull;
+          v1[i][p] = in(i) ? add_f32x2(v1[i][p], m1) : 0ull;
         }
     }
     float q0 = squares(v0), q1 = squares(v1);
@@ -607,7 +616,7 @@ __global__ void __launch_bounds__(norm_gate_threads<NV>(), 1)
   auto put = [&](T* out, size_t r, const Row& v) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      *reinterpret_cast<uint4*>(out + r * a.d + static_cast<size_t>(i * tsize + t) * E) = pack_pairs(v[i]);
+      if (in(i)) *reinterpret_cast<uint4*>(out + r * a.d + static_cast<size_t>(i * tsize + t) * E) = pack_pairs(v[i]);
   };
   int s = 0;
   uint32_t phase = 0;
@@ -622,8 +631,9 @@ __global__ void __launch_bounds__(norm_gate_threads<NV>(), 1)
     Row v0, v1;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      unpack_pairs<T>(*reinterpret_cast<const uint4*>(ys + i * tsize * 16), v0[i]);
-      unpack_pairs<T>(*reinterpret_cast<const uint4*>(ys + rowbytes + i * tsize * 16), v1[i]);
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      unpack_pairs<T>(in(i) ? *reinterpret_cast<const uint4*>(ys + i * tsize * 16) : zero, v0[i]);
+      unpack_pairs<T>(in(i) ? *reinterpret_cast<const uint4*>(ys + rowbytes + i * tsize * 16) : zero, v1[i]);
     }
     fence_proxy_async_smem();
     ok = team_all(here);                   // and every thread has read y
@@ -634,7 +644,7 @@ __global__ void __launch_bounds__(norm_gate_threads<NV>(), 1)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       uint64_t r[P];
-      unpack_pairs<T>(*reinterpret_cast<const uint4*>(xs + i * tsize * 16), r);
+      unpack_pairs<T>(in(i) ? *reinterpret_cast<const uint4*>(xs + i * tsize * 16) : make_uint4(0, 0, 0, 0), r);
 #pragma unroll
       for (int p = 0; p < P; ++p) v0[i][p] = fma_f32x2(gs[i][p], v0[i][p], r[p]);
     }
@@ -642,7 +652,7 @@ __global__ void __launch_bounds__(norm_gate_threads<NV>(), 1)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       uint64_t r[P];
-      unpack_pairs<T>(*reinterpret_cast<const uint4*>(xs + rowbytes + i * tsize * 16), r);
+      unpack_pairs<T>(in(i) ? *reinterpret_cast<const uint4*>(xs + rowbytes + i * tsize * 16) : make_uint4(0, 0, 0, 0), r);
 #pragma unroll
       for (int p = 0; p < P; ++p) v1[i][p] = fma_f32x2(gs[i][p], v1[i][p], r[p]);
     }
@@ -652,6 +662,7 @@ __global__ void __launch_bounds__(norm_gate_threads<NV>(), 1)
     if (g0 >= 0) put(x_out, row, v0);
     if (g1 >= 0) put(x_out, row + 1, v1);
     if (a.pre_g) {
+      // (behind the end of a ragged row x' is zero here, as y, x and the vectors are)
       norm2(v0, v1, 2, true);
       if (Q8 == ROW_T) {
         if (g0 >= 0) put(xn, row, v0);
@@ -693,7 +704,7 @@ __global__ void __launch_bounds__(norm_gate_threads<NV>(), 1)
     }
 }
 
-// any d (fp32 rows): one warp per row, scalar.  Only the lane that holds a column
+// fp32 rows wider than a team: one warp per row, scalar.  Only the lane that holds a column
 // reads or writes it, so x' may replace x and serves as the row's storage between
 // the two norms.
 __global__ void __launch_bounds__(256) norm_gate_generic_kernel(const float* x, const float* y, float* x_out, float* xn,

@@ -208,14 +208,14 @@ static cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
   cfg.numAttrs = 1;
   // one shared-memory carve-out for every hot kernel, so that consecutive kernels
   // never wait for the SM to re-partition L1 and shared memory
-  static thread_local const void* seen[64];
+  static thread_local const void* seen[256];
   static thread_local int nseen = 0;
   const void* key = reinterpret_cast<const void*>(kern);
   bool known = false;
   for (int i = 0; i < nseen; ++i) known |= seen[i] == key;
   if (!known) {
     cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-    if (nseen < 64) seen[nseen++] = key;
+    if (nseen < 256) seen[nseen++] = key;
   }
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
@@ -484,9 +484,10 @@ static ts_status launch_norm_gate_nv(const void* x, const void* y, void* x_out, 
   }
   // as many teams as a block's registers, shared memory and (several warps a team) named barriers hold, or as the rows
   // give work to; then as many pairs of rows on their way as fit
-  const int team_warps = a.d / (32 * ts::Vec<T>::E * NV);
+  constexpr int VEC = 32 * ts::Vec<T>::E * NV;    // columns of a warp
+  const int team_warps = (a.d + VEC - 1) / VEC;
   const unsigned pairs = static_cast<unsigned>((static_cast<size_t>(a.rows) + 1) / 2), sms = num_sms();
-  const size_t pair = 4 * static_cast<size_t>(a.d) * sizeof(T), vecs = 16 * static_cast<size_t>(a.d);
+  const size_t pair = 4 * static_cast<size_t>(a.d) * sizeof(T), vecs = 16 * static_cast<size_t>(VEC) * team_warps;
   size_t teams = ts::norm_gate_threads<NV>() / (32 * team_warps);
   teams = std::min(teams, (kNormGateSmem - vecs) / pair);
   teams = std::min<size_t>(teams, team_warps > 1 ? 15 : ts::kNormGateTeams);
@@ -500,21 +501,23 @@ static ts_status launch_norm_gate_nv(const void* x, const void* y, void* x_out, 
 }
 
 // Few rows (at most two pairs for each block that is resident at once): a block per pair of rows.  Else vectors per
-// thread: the most, up to four, that divide the row among whole warps.
+// thread: the most, up to four, that divide the row among whole warps (fp32 rows, of any multiple of four columns: that
+// leave at most a fifth of the team's vectors behind the end of the row).
 template <typename T, int Q8>
 static ts_status launch_norm_gate(const void* x, const void* y, void* x_out, void* xn, uint8_t* q8, float* qs,
                                   const ts::NormGateArgs& a, cudaStream_t st) {
-  const int k = a.d / (32 * ts::Vec<T>::E);
-  const long pairs = (static_cast<long>(a.rows) + 1) / 2, blocks = static_cast<long>(16 / k) * num_sms();
+  const int k = (a.d + 32 * ts::Vec<T>::E - 1) / (32 * ts::Vec<T>::E);    // warps with one vector in each thread
+  const long pairs = (static_cast<long>(a.rows) + 1) / 2, blocks = k <= 8 ? static_cast<long>(16 / k) * num_sms() : 0;
   if (pairs <= 2 * blocks) {
     trace_pre(st);
     launch_pdl(ts::norm_gate_few_kernel<T, Q8>, dim3(static_cast<unsigned>(std::min(pairs, blocks))), dim3(32 * k), 0, st,
                static_cast<const T*>(x), static_cast<const T*>(y), static_cast<T*>(x_out), static_cast<T*>(xn), q8, qs, a);
     return trace_post(st, "norm_gate");
   }
-  if (k % 4 == 0) return launch_norm_gate_nv<T, 4, Q8>(x, y, x_out, xn, q8, qs, a, st);
-  if (k % 3 == 0) return launch_norm_gate_nv<T, 3, Q8>(x, y, x_out, xn, q8, qs, a, st);
-  if (k % 2 == 0) return launch_norm_gate_nv<T, 2, Q8>(x, y, x_out, xn, q8, qs, a, st);
+  auto fits = [&](int nv) { return sizeof(T) == 4 ? 4 * nv * ((k + nv - 1) / nv) <= 5 * k : k % nv == 0; };
+  if (fits(4)) return launch_norm_gate_nv<T, 4, Q8>(x, y, x_out, xn, q8, qs, a, st);
+  if (fits(3)) return launch_norm_gate_nv<T, 3, Q8>(x, y, x_out, xn, q8, qs, a, st);
+  if (fits(2)) return launch_norm_gate_nv<T, 2, Q8>(x, y, x_out, xn, q8, qs, a, st);
   return launch_norm_gate_nv<T, 1, Q8>(x, y, x_out, xn, q8, qs, a, st);
 }
 
@@ -540,7 +543,7 @@ static ts_status run_norm_gate(const ts_model_desc* m, const ts_norm_gate* p, co
   const double e = esize(m->dtype);
   set_work("norm_gate", 0.0, static_cast<double>(rows) * m->d * (3.0 * e + (p->pre_g ? (q8 ? 1.0 : e) : 0.0)));
   if (m->dtype == TS_F32) {
-    if (m->d % 128 == 0 && m->d <= 1024)
+    if (m->d <= 4096)      // eight warps of four vectors
       return launch_norm_gate<float, ts::ROW_T>(x, y, x_out, xn, nullptr, nullptr, a, st);
     trace_pre(st);
     ts::norm_gate_generic_kernel<<<rows_grid(rows), 256, 0, st>>>(static_cast<const float*>(x), static_cast<const float*>(y),

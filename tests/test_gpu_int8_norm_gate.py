@@ -162,25 +162,30 @@ def test_integer_sums_are_exact_at_their_largest(M):
     check_linear(M, K, N, "bias", x=x, sx=np.full(M, 2.0 ** -20), wq=wq, sw=np.full(N, 2.0 ** -6))
 
 
-def test_rows_that_are_not_finite_stay_apart():
+@pytest.mark.parametrize("M,K", [(9, 256), (20, 256), (200, 1024), (2500, 256)])
+@pytest.mark.parametrize("epi", ["bias", "gelu", "swiglu", "resid"])
+def test_rows_that_are_not_finite_stay_apart(M, K, epi):
+    """A NaN or an infinity in a row makes that row's outputs NaN, through every epilogue and kernel, and no other's."""
     rng = np.random.default_rng(5)
-    M, K, N = 9, 256, 128
+    N = 128
+    wide = 2 * N if epi == "swiglu" else N
     x = W.round_to(rng.standard_normal((M, K)), "bf16")
     x[2] = 0.0
     xb = torch.from_numpy(x).to("cuda", torch.bfloat16)
     xb[4, 7] = float("inf")
     xb[6, 0] = float("nan")
-    wq = rng.integers(-127, 128, (N, K))
-    sw = np.full(N, 2.0 ** -10)
-    y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    wq = rng.integers(-127, 128, (wide, K))
+    sw = np.full(wide, 2.0 ** -10)
+    y = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
     scratch = torch.empty(M * K + 4 * M, dtype=torch.uint8, device="cuda")
-    b = W.round_to(rng.standard_normal(N), "f32")
-    B.op_linear(model(), xb, i8(wq), dev(b, torch.float32), y, w_scale=dev(sw, torch.float32), scratch=scratch)
+    b = W.round_to(rng.standard_normal(wide), "f32")
+    B.op_linear(model("rms_swiglu" if epi == "swiglu" else "ln_gelu"), xb, i8(wq), dev(b, torch.float32), y, EPIS[epi],
+                w_scale=dev(sw, torch.float32), scratch=scratch)
     got = host(y)
     assert np.isnan(got[[4, 6]]).all()
-    rows = [0, 1, 2, 3, 5, 7, 8]
+    rows = [r for r in range(M) if r not in (4, 6)]
     q, s = I8.quantize_rows(x)
-    want, tol = linear_reference(q, s, wq, sw, b, "bias")
+    want, tol = linear_reference(q, s, wq, sw, b, epi, np.zeros((M, N)))
     assert (np.abs(got[rows] - want[rows]) <= tol[rows]).all()
 
 
@@ -275,7 +280,10 @@ SEAMS = [(1, 256, 4, "bf16", 1), (7, 1536, 24, "bf16", 3), (33, 512, 8, "bf16", 
 # rows enough for the kernel of many rows, at every number of vectors per thread and of warps per row
 MANY = [(9601, 256, 4, "bf16", 3), (4802, 512, 8, "bf16", 2), (3001, 768, 12, "bf16", 1), (2501, 1024, 16, "bf16", 4),
         (1903, 1280, 20, "bf16", 2), (1301, 1536, 24, "bf16", 3), (1280, 1792, 28, "bf16", 2), (1251, 2048, 32, "bf16", 5),
-        (2501, 512, 8, "f32", 2), (1301, 1024, 16, "f32", 3), (1303, 896, 14, "f32", 1)]
+        (2501, 512, 8, "f32", 2), (1301, 1024, 16, "f32", 3), (1303, 896, 14, "f32", 1),
+        # fp32 rows that end inside a team's vectors, one wider than a block of few rows, one wider than a team
+        (9601, 48, 3, "f32", 2), (5001, 240, 15, "f32", 3), (2501, 592, 37, "f32", 2), (1301, 1008, 63, "f32", 1),
+        (700, 2064, 129, "f32", 2), (3, 4096, 64, "f32", 1), (5, 4160, 65, "f32", 2)]
 
 
 @pytest.mark.parametrize("rows,d,heads,dtype,groups", SEAMS + MANY)
@@ -342,7 +350,8 @@ def test_norm_gate_e4m3_rows(rows):
     assert (np.abs(v - n1) <= 2.0 ** -4 * (np.abs(n1) + dn) + 2.0 ** -10 * host(xs)[:, None] + dn).all()
 
 
-@pytest.mark.parametrize("rows,d,heads,dtype", [(40, 512, 8, "bf16"), (40, 48, 3, "f32"), (2501, 1024, 16, "bf16")])
+@pytest.mark.parametrize("rows,d,heads,dtype", [(40, 512, 8, "bf16"), (40, 48, 3, "f32"), (2501, 1024, 16, "bf16"),
+                                                (40, 4160, 65, "f32")])
 def test_norm_gate_group_out_of_range_is_reported_and_leaves_the_row(rows, d, heads, dtype):
     c = Seam(rows, d, heads, dtype, "ln_gelu", 3)
     c.group[[7, 31]] = [3, -1]
@@ -632,3 +641,127 @@ def test_calls_with_no_rows_do_nothing():
     x = none(256, torch.bfloat16)
     B.op_norm_gate(model(), B.norm_gate_desc(), x, x, x)
     assert B.launch_count() == n
+
+
+# ---------------------------------------------------------------------------
+# calls that come first, large offsets, threads
+# ---------------------------------------------------------------------------
+FIRST_CAPTURE = '''
+import numpy as np, torch
+from shared_token_transformer_b200 import binding as B
+m = B.model_desc(256, 4, 256, "int8", (0, 32, 32))
+def call(M, K, N):
+    x = torch.ones((M, K), dtype=torch.bfloat16, device="cuda")
+    w = torch.ones((N, K), dtype=torch.int8, device="cuda")
+    s, b = torch.full((N,), 1.0 / 127, device="cuda"), torch.zeros(N, device="cuda")
+    y = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+    sc = torch.zeros(M * (K + 4), dtype=torch.uint8, device="cuda")
+    return (lambda: B.op_linear(m, x, w, b, y, w_scale=s, scratch=sc)), y, K / 127, (x, w, s, b, y, sc)
+def seam(M):
+    x = torch.ones((M, 256), dtype=torch.bfloat16, device="cuda")
+    o, g = torch.zeros_like(x), B.norm_gate_desc(scale=torch.full((256,), 2.0, device="cuda"))
+    return (lambda: B.op_norm_gate(m, g, x, x, o)), o, 3.0, (x, o, g)
+# one row (blocks quantise), few rows, a cluster that shares K, whole tiles, pairs of SMs; few and many rows of the seam
+calls = [call(1, 256, 64), call(20, 256, 64), call(128, 2048, 128), call(2500, 256, 256), call(6000, 512, 2048), seam(3), seam(9601)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    for f, *_ in calls:
+        f()
+g.replay()
+torch.cuda.synchronize()
+B.device_status()
+for f, y, want, _ in calls:
+    assert (y.double() - want).abs().max().item() <= want * 2.0 ** -8, (y.shape, want, y.flatten()[:4])
+print("captured first")
+'''
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CAPTURE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, (r.stdout, r.stderr[-2000:])
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows of the quantiser, the seam and the product are those of a small call."""
+    d, rows, tail = 1024, (1 << 21) + 37, 70
+    rng = np.random.default_rng(2)
+    c = Seam(tail, d, 16, "int8", "ln_gelu", 1)
+    x, y = (torch.zeros((rows, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x[-tail:], y[-tail:] = dev(c.x, c.dt), dev(c.y, c.dt)
+    gates = B.norm_gate_desc(**{k: dev(a, torch.float32) for k, a in c.v.items()})
+    xn, xs = torch.empty((rows, d), dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
+    small_n, small_s = torch.empty((tail, d), dtype=torch.int8, device="cuda"), torch.empty(tail, device="cuda")
+    small_x = torch.empty((tail, d), dtype=torch.bfloat16, device="cuda")
+    B.op_norm_gate(c.m, gates, x, y, x, xn, xs)
+    B.op_norm_gate(c.m, gates, dev(c.x, c.dt), dev(c.y, c.dt), small_x, small_n, small_s)
+    # the two kernels sum in different orders: x' within a bf16 step, integers within one
+    assert ((x[-tail:] - small_x).abs() <= 2.0 ** -7 * small_x.abs() + 1e-6).all()
+    assert ((xn[-tail:].int() - small_n.int()).abs() <= 1).all()
+    assert torch.allclose(xs[-tail:], small_s, rtol=1e-4, atol=0)
+    q, s = torch.empty((rows, d), dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
+    B.quantize_rows_i8(x, q, s)
+    want_q, want_s = I8.quantize_rows(host(x[-tail:]))
+    np.testing.assert_array_equal(host(q[-tail:]), want_q)
+    np.testing.assert_array_equal(host(s[-tail:]), want_s)
+    del x, y, xn
+    N = 1032
+    wq, sw, b = i8(rng.integers(-127, 128, (N, d))), torch.full((N,), 2.0 ** -12, device="cuda"), torch.zeros(N, device="cuda")
+    out, small = torch.empty((rows, N), dtype=torch.bfloat16, device="cuda"), torch.empty((tail, N), dtype=torch.bfloat16, device="cuda")
+    B.op_linear_q8(model(), q, s, wq, sw, b, out)
+    B.op_linear_q8(model(), q[-tail:].clone(), s[-tail:].clone(), wq, sw, b, small)
+    assert torch.equal(out[-tail:], small)
+
+
+def test_host_threads_at_once_agree():
+    """Two host threads on streams of their own, each with its own buffers."""
+    import threading
+    rng = np.random.default_rng(9)
+    K, N = 512, 520
+    wq, sw, b = i8(rng.integers(-127, 128, (N, K))), torch.full((N,), 2.0 ** -12, device="cuda"), torch.zeros(N, device="cuda")
+    xs = [dev(rng.standard_normal((M, K)), torch.bfloat16) for M in (3, 130)]
+    want = []
+    for x in xs:
+        y = torch.empty((x.shape[0], N), dtype=torch.bfloat16, device="cuda")
+        B.op_linear(model(), x, wq, b, y, w_scale=sw, scratch=torch.empty(x.shape[0] * (K + 4), dtype=torch.uint8, device="cuda"))
+        want.append(y)
+    torch.cuda.synchronize()
+    got, errors = [torch.zeros_like(y) for y in want], []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            scratch = torch.empty(xs[i].shape[0] * (K + 4), dtype=torch.uint8, device="cuda")
+            for _ in range(100):
+                B.op_linear(model(), xs[i], wq, b, got[i], w_scale=sw, scratch=scratch, stream=s)
+            s.synchronize()
+        except Exception as e:      # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    assert all(torch.equal(a, w) for a, w in zip(got, want))
+
+
+@pytest.mark.parametrize("mode", [B.TS_ROWS_SHARED, B.TS_ROWS_TILED])
+def test_int8_qkv_values(mode):
+    """The v part of op_qkv is the int8 linear layer of Norm1 (q and k pass the norm and rotation of every dtype)."""
+    c = Layers(SMALL)
+    state = c.S if mode == B.TS_ROWS_SHARED else OL.gather(c.S, c.op).reshape(-1, SMALL.d)
+    rows, d = state.shape
+    qkv = torch.empty((rows, 3 * d), dtype=torch.bfloat16, device="cuda")
+    B.op_qkv(c.plan, c.m, c.w[0], mode, dev(state, c.dt), qkv, torch.empty(rows * d * 6 + 8192, dtype=torch.uint8, device="cuda"))
+    q, k, v = OL.qkv_project(state, c.p[0], c.om)
+    assert rel_l2(host(qkv)[:, 2 * d:], v.reshape(rows, d)) < TOL["int8"]
+    # rotation keeps each head's norm
+    for part, want in ((0, q), (1, k)):
+        got = host(qkv)[:, part * d:(part + 1) * d].reshape(rows, SMALL.heads, -1)
+        assert rel_l2(np.linalg.norm(got, axis=2), np.linalg.norm(want, axis=2)) < TOL["int8"]
