@@ -135,7 +135,9 @@ SIZES = [(1, 16, 8), (1, 1536, 4608), (2, 64, 64), (6, 6144, 1536), (9, 80, 72),
          (33, 512, 2048), (64, 1536, 520), (65, 1040, 1336), (127, 96, 264), (128, 128, 128), (129, 256, 192),
          (257, 4096, 1024), (333, 1040, 1336), (777, 2048, 512), (2320, 512, 1000), (4099, 272, 776),
          # clusters of two to six CTAs share K: 333, 257, 300, 600 and 64 rows, and a K of fewer slices than CTAs
-         (300, 1024, 768), (600, 2048, 264), (40, 6144, 520), (50, 272, 24), (250, 400, 1000)]
+         (300, 1024, 768), (600, 2048, 264), (40, 6144, 520), (50, 272, 24), (250, 400, 1000),
+         # up to 64 rows of a wide W: one CTA a tile
+         (33, 2048, 8192), (64, 1040, 5000)]
 
 
 @pytest.mark.parametrize("M,K,N", SIZES)
