@@ -248,21 +248,23 @@ def layer_weights(tensors):
 
 def _keep(struct, tensors):
     """Fill a struct of fp32 vectors [d], gates [groups, d] and an int32 row_group, and keep the tensors alive."""
-    width, groups = set(), set()
+    width, groups, device = set(), set(), set()
     for n, t in tensors.items():
         if t is None:
             continue
         if not t.is_contiguous() or t.itemsize != 4:
             raise ValueError(f"{n} must be contiguous with elements of 32 bits")
         setattr(struct, n, t.data_ptr())
+        device.add(t.get_device())
         if n.startswith("gate"):
             groups.add(t.shape[0])
         if n != "row_group":
             width.add(t.shape[-1])
-    if len(groups) > 1 or len(width) > 1:
-        raise ValueError("the vectors have different widths or the gates different numbers of groups")
+    if len(groups) > 1 or len(width) > 1 or len(device) > 1:
+        raise ValueError("the vectors have different widths or devices, or the gates different numbers of groups")
     struct.groups = groups.pop() if groups else 0
     struct.width = width.pop() if width else 0
+    struct.device = device.pop() if device else None
     struct._tensors = dict(tensors)
     return struct
 
@@ -309,8 +311,9 @@ def block_partial(plan, model, weights, shared_ops, X, ws, stream=None):
 
 def _sandwich_rows(fn, model, sandwich, rows):
     group = sandwich._tensors.get("row_group")
-    if sandwich.width not in (model.d, 0) or (group is not None and group.numel() != rows):
-        raise TileShareError(fn, 1, f"sandwich vectors of width {sandwich.width} or a row_group that is not of {rows} rows")
+    if (sandwich.width not in (model.d, 0) or sandwich.device not in ((_device or _cuda())(), None) or
+            (group is not None and group.numel() != rows)):
+        raise TileShareError(fn, 1, f"sandwich vectors of another width or device, or a row_group not of {rows} rows")
 
 
 def block_shared_sandwich(plan, model, weights, sandwich, S, ws, stream=None):
@@ -402,15 +405,17 @@ def op_norm_gate(model, gates, x, y, x_out, xn=None, xn_scale=None, row_group=No
     """ts_op_norm_gate: x_out = x + gate * scale * Norm_post(y) and xn = Norm_pre(x_out), as 8-bit rows with xn_scale."""
     rows, d = x.shape
     e = 4 if model.dtype == TS_F32 else 2
-    if not (d == model.d and gates.width in (d, 0) and x.nbytes == y.nbytes == rows * d * e <= x_out.nbytes and
+    device = (_device or _cuda())()
+    if not (d == model.d and gates.width in (d, 0) and gates.device in (device, None) and x.nbytes == y.nbytes == rows * d * e <= x_out.nbytes and
             x_out.itemsize == e and x.is_contiguous() and y.is_contiguous() and x_out.is_contiguous() and
-            x.get_device() == x_out.get_device() == (_device or _cuda())()):
+            x.get_device() == y.get_device() == x_out.get_device() == device):
         _unfit("ts_op_norm_gate")
-    if xn is not None and not (xn.is_contiguous() and xn.itemsize == (e if xn_scale is None else 1) and
+    if xn is not None and not (xn.is_contiguous() and xn.get_device() == device and xn.itemsize == (e if xn_scale is None else 1) and
                                xn.nbytes >= rows * d * xn.itemsize and
-                               (xn_scale is None or xn_scale.nbytes >= 4 * rows)):
+                               (xn_scale is None or (xn_scale.nbytes >= 4 * rows and
+                                                     xn_scale.get_device() == device))):
         _unfit("ts_op_norm_gate")
-    if row_group is not None and row_group.nbytes != 4 * rows:
+    if row_group is not None and (row_group.nbytes != 4 * rows or row_group.get_device() != device):
         _unfit("ts_op_norm_gate")
     status = (_lib or lib()).ts_op_norm_gate(ctypes.byref(model), ctypes.byref(gates), x.data_ptr(), y.data_ptr(),
                                              _ptr(row_group), rows, x_out.data_ptr(), _ptr(xn), _ptr(xn_scale),
@@ -427,7 +432,8 @@ def op_linear(model, x, W, bias, y, epi=TS_EPI_BIAS, w_scale=None, scratch=None,
             x.nbytes == 2 * rows * K and W.nbytes == wide * K and y.nbytes >= 2 * rows * N and y.itemsize == 2 and
             w_scale is not None and scratch is not None and bias.nbytes >= 4 * wide <= w_scale.nbytes and
             scratch.nbytes >= rows * (K + 4) and x.is_contiguous() and W.is_contiguous() and y.is_contiguous() and
-            x.get_device() == y.get_device() == (_device or _cuda())()):
+            x.get_device() == y.get_device() == W.get_device() == bias.get_device() == w_scale.get_device() ==
+            scratch.get_device() == (_device or _cuda())()):
         _unfit("ts_op_linear")
     status = (_lib or lib()).ts_op_linear(ctypes.byref(model), x.data_ptr(), rows, K, W.data_ptr(), _ptr(w_scale), N,
                                           _ptr(bias), epi, y.data_ptr(), _ptr(scratch), _stream(stream))
@@ -443,7 +449,8 @@ def op_linear_q8(model, x, x_scale, W, w_scale, bias, y, epi=TS_EPI_BIAS, stream
     if not (x.nbytes == rows * K and W.nbytes == wide * K and y.nbytes >= 2 * rows * N and y.itemsize == 2 and
             bias.nbytes >= 4 * wide <= w_scale.nbytes and x_scale.nbytes >= 4 * rows and x.is_contiguous() and
             W.is_contiguous() and y.is_contiguous() and
-            x.get_device() == y.get_device() == (_device or _cuda())()):
+            x.get_device() == y.get_device() == W.get_device() == bias.get_device() == w_scale.get_device() ==
+            x_scale.get_device() == (_device or _cuda())()):
         _unfit("ts_op_linear_q8")
     status = (_lib or lib()).ts_op_linear_q8(ctypes.byref(model), x.data_ptr(), x_scale.data_ptr(), rows, K,
                                              W.data_ptr(), w_scale.data_ptr(), N, bias.data_ptr(), epi, y.data_ptr(),

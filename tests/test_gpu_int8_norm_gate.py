@@ -608,13 +608,15 @@ def test_binding_refuses_tensors_that_do_not_fit():
     wide = torch.zeros((M, 2 * K), dtype=torch.int8, device="cuda")
     for bad in ({"x": wide[:, :K]}, {"x": x[::2].t().contiguous()[:, :4]}, {"W": w.t()}, {"W": w[:, :64]}, {"x": x.cpu()},
                 {"x": xb}, {"y": y.float()}, {"y": y[: M - 1]}, {"bias": b[: N - 1]}, {"w_scale": s[:8]},
-                {"x_scale": s[: M - 1]}, {"W": w.bfloat16()}, {"y": y.t()}):
+                {"x_scale": s[: M - 1]}, {"W": w.bfloat16()}, {"y": y.t()}, {"bias": b.cpu()}, {"w_scale": s.cpu()},
+                {"x_scale": s.cpu()}, {"W": w.cpu()}, {"y": y.cpu()}):
         with pytest.raises(B.TileShareError) as e:
             B.op_linear_q8(**dict(ok, **bad))
         assert e.value.status == 1
     lin = dict(model=model(), x=xb, W=w, bias=b, y=y, w_scale=s, scratch=scratch)
     B.op_linear(**lin)
-    for bad in ({"x": x}, {"scratch": scratch[:-1]}, {"scratch": None}, {"w_scale": None}, {"W": w[:, ::2]}, {"x": xb[:, ::2]}):
+    for bad in ({"x": x}, {"scratch": scratch[:-1]}, {"scratch": None}, {"w_scale": None}, {"W": w[:, ::2]}, {"x": xb[:, ::2]},
+                {"scratch": scratch.cpu()}, {"bias": b.cpu()}):
         with pytest.raises(B.TileShareError) as e:
             B.op_linear(**dict(lin, **bad))
         assert e.value.status == 1
@@ -627,6 +629,12 @@ def test_binding_refuses_tensors_that_do_not_fit():
         c.call(x1, x1.to(torch.int8))                      # 8-bit rows need their scales
     with pytest.raises(B.TileShareError):                  # vectors of another width
         B.op_norm_gate(c.m, B.norm_gate_desc(scale=torch.ones(128, device="cuda")), x1, x1, x1)
+    for bad in ({"gates": B.norm_gate_desc(scale=torch.ones(256))}, {"y": x1.cpu()},
+                {"row_group": torch.zeros(M, dtype=torch.int32)}, {"row_group": torch.zeros(M, dtype=torch.int64, device="cuda")}):
+        with pytest.raises(B.TileShareError):
+            B.op_norm_gate(**dict(dict(model=c.m, gates=B.norm_gate_desc(), x=x1, y=x1, x_out=x1), **bad))
+    with pytest.raises(ValueError):
+        B.norm_gate_desc(scale=torch.ones(256), gate=torch.ones((1, 256), device="cuda"))
     q = torch.empty((M, K), dtype=torch.int8, device="cuda")
     for args in ((xb, q[:-1], s), (xb.t(), q, s), (xb.float(), q, s), (xb, q, s[:4])):
         with pytest.raises(B.TileShareError):
