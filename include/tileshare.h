@@ -201,7 +201,7 @@ typedef struct {
   const float* post2_g; const float* post2_b;  /* [d] norm after the MLP            */
   const float* gate2;   const float* scale2;   /* [groups, d], [d]                  */
   const int* row_group; /* [rows of the state] gate row of each state row, in [0, groups);
-                           NULL: gate row 0 for all (see ts_norm_gate)               */
+                           NULL: gate row 0 for all (see ts_op_norm_gate)            */
   int groups;
 } ts_sandwich_weights;
 

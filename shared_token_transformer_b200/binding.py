@@ -417,9 +417,11 @@ def op_norm_gate(model, gates, x, y, x_out, xn=None, xn_scale=None, row_group=No
         _unfit("ts_op_norm_gate")
     if row_group is not None and (row_group.nbytes != 4 * rows or row_group.get_device() != device):
         _unfit("ts_op_norm_gate")
-    status = (_lib or lib()).ts_op_norm_gate(ctypes.byref(model), ctypes.byref(gates), x.data_ptr(), y.data_ptr(),
-                                             _ptr(row_group), rows, x_out.data_ptr(), _ptr(xn), _ptr(xn_scale),
-                                             _stream(stream))
+    status = (_lib or lib()).ts_op_norm_gate(
+        ctypes.byref(model), ctypes.byref(gates), x.data_ptr(), y.data_ptr(),
+        None if row_group is None else row_group.data_ptr(), rows, x_out.data_ptr(),
+        None if xn is None else xn.data_ptr(), None if xn_scale is None else xn_scale.data_ptr(),
+        _raw_stream(device) if stream is None else stream.cuda_stream)
     if status:
         _check("ts_op_norm_gate", status)
 
@@ -446,15 +448,16 @@ def op_linear_q8(model, x, x_scale, W, w_scale, bias, y, epi=TS_EPI_BIAS, stream
     rows, K = x.shape
     wide = W.shape[0]
     N = wide // 2 if epi == TS_EPI_BIAS_SWIGLU else wide     # output width
+    device = (_device or _cuda())()
     if not (x.nbytes == rows * K and W.nbytes == wide * K and y.nbytes >= 2 * rows * N and y.itemsize == 2 and
             bias.nbytes >= 4 * wide <= w_scale.nbytes and x_scale.nbytes >= 4 * rows and x.is_contiguous() and
             W.is_contiguous() and y.is_contiguous() and
             x.get_device() == y.get_device() == W.get_device() == bias.get_device() == w_scale.get_device() ==
-            x_scale.get_device() == (_device or _cuda())()):
+            x_scale.get_device() == device):
         _unfit("ts_op_linear_q8")
     status = (_lib or lib()).ts_op_linear_q8(ctypes.byref(model), x.data_ptr(), x_scale.data_ptr(), rows, K,
                                              W.data_ptr(), w_scale.data_ptr(), N, bias.data_ptr(), epi, y.data_ptr(),
-                                             _stream(stream))
+                                             _raw_stream(device) if stream is None else stream.cuda_stream)
     if status:
         _check("ts_op_linear_q8", status)
 
