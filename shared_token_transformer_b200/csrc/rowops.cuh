@@ -188,8 +188,9 @@ __global__ void __launch_bounds__(256) layernorm_generic_kernel(const T* __restr
 // registers allow: a team of one warp (two for wide rows, more where only that divides
 // the row) takes two rows at a time, NV 16-byte vectors of each in a thread, and each
 // reduction, barrier and read of the gains and biases in shared memory serves both rows.
-// Rows arrive by bulk copy without registers; the copy of the next y starts when this
-// one is in registers, that of the next x when x' is formed.
+// Rows arrive by bulk copy without registers; the copy of a team's next y starts when
+// this one is in registers, that of its next x when x' is formed (a deeper queue was no
+// faster: the block's other teams fill the waits).
 // ---------------------------------------------------------------------------
 struct NormGateArgs {
   int rows, d, groups, rms;
@@ -422,8 +423,8 @@ __global__ void __launch_bounds__(256) norm_gate_few_kernel(const T* x, const T*
 
 constexpr int kNormGateTeamWarps = 8;    // most warps of a team
 constexpr int kNormGateTeams = 32;       // most teams of a block
-constexpr int kNormGateStages = 4;       // most pairs of rows on their way to a team
-// most threads of a block by the registers that NV vectors of two rows take
+// most threads of a block by the registers that NV vectors of two rows take (fp32 vectors take half as many, but more
+// warps a block were slower there: 20000 x 1024 68 us with 640 threads, 55 with 384)
 template <int NV>
 constexpr int norm_gate_threads() {
   return NV == 1 ? 896 : NV == 2 ? 640 : NV == 3 ? 512 : 384;
@@ -432,10 +433,10 @@ constexpr int norm_gate_threads() {
 template <typename T, int NV, int Q8>
 __global__ void __launch_bounds__(norm_gate_threads<NV>(), 1)
     norm_gate_kernel(const T* x, const T* y, T* x_out, T* xn, uint8_t* q8, float* qscale, const NormGateArgs a,
-                     int team_warps, int stages) {
-  extern __shared__ __align__(128) uint8_t smem[];    // vectors [4][d], then per team stages x (2 rows of y, 2 of x)
+                     int team_warps) {
+  extern __shared__ __align__(128) uint8_t smem[];    // vectors [4][d], then per team two rows of y and two of x
   __shared__ __align__(16) float red[kNormGateTeams][2][2][kNormGateTeamWarps];
-  __shared__ __align__(8) uint64_t bars[kNormGateTeams][kNormGateStages][2];    // y, x
+  __shared__ __align__(8) uint64_t bars[kNormGateTeams][2];    // y, x
   constexpr int E = Vec<T>::E, P = E / 2, Q = E / 4;
   constexpr bool RAGGED = sizeof(T) == 4;    // fp32 rows may end inside a team's vectors: what lies behind is zero
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % team_warps, team = (threadIdx.x >> 5) / team_warps;
@@ -444,12 +445,10 @@ __global__ void __launch_bounds__(norm_gate_threads<NV>(), 1)
   const float inv_d = 1.0f / static_cast<float>(a.d);
   const int quads = RAGGED ? NV * Q * tsize : a.d / 4;    // four-column quads of a vector in shared memory
   auto in = [&](int i) -> bool { return !RAGGED || (i * tsize + t) * E < a.d; };
-  uint8_t* ring = smem + static_cast<size_t>(64) * quads + static_cast<size_t>(team) * stages * 4 * rowbytes;
+  uint8_t* ring = smem + static_cast<size_t>(64) * quads + static_cast<size_t>(team) * 4 * rowbytes;
   if (t == 0) {
-    for (int s = 0; s < stages; ++s) {
-      mbar_init(smem_u32(&bars[team][s][0]), 1);
-      mbar_init(smem_u32(&bars[team][s][1]), 1);
-    }
+    mbar_init(smem_u32(&bars[team][0]), 1);
+    mbar_init(smem_u32(&bars[team][1]), 1);
     fence_barrier_init();
   }
   if (t < 32) (&red[team][0][0][0])[t] = 0.f;    // warps that a team lacks add nothing
@@ -470,17 +469,16 @@ __global__ void __launch_bounds__(norm_gate_threads<NV>(), 1)
   pdl_trigger();
   const size_t rows = a.rows, step = 2 * static_cast<size_t>(gridDim.x) * teams;
   size_t row = 2 * (static_cast<size_t>(blockIdx.x) * teams + team);
-  // copy of a pair of rows of y (k = 0) or x (k = 1) into stage s, by one thread of the team
-  auto issue = [&](int s, int k, size_t r) {
-    const uint32_t n = r + 1 < rows ? 2 * rowbytes : rowbytes, bar = smem_u32(&bars[team][s][k]);
+  // copy of a pair of rows of y (k = 0) or x (k = 1), by one thread of the team
+  auto issue = [&](int k, size_t r) {
+    const uint32_t n = r + 1 < rows ? 2 * rowbytes : rowbytes, bar = smem_u32(&bars[team][k]);
     mbar_expect_tx(bar, n);
-    bulk_load(smem_u32(ring) + static_cast<uint32_t>(4 * s + 2 * k) * rowbytes, (k ? x : y) + r * a.d, n, bar);
+    bulk_load(smem_u32(ring) + static_cast<uint32_t>(2 * k) * rowbytes, (k ? x : y) + r * a.d, n, bar);
   };
-  if (t == 0)
-    for (int s = 0; s < stages && row + s * step < rows; ++s) {
-      issue(s, 0, row + s * step);
-      issue(s, 1, row + s * step);
-    }
+  if (t == 0 && row < rows) {
+    issue(0, row);
+    issue(1, row);
+  }
   // The shared vectors.  Thread t owns vectors i * tsize + t of a row; the four-column quads of a vector lie tsize
   // float4s apart, so that a warp reads them without bank conflicts.
   const float* src[4] = {a.post_g, a.rms ? nullptr : a.post_b, a.pre_g, a.rms ? nullptr : a.pre_b};
@@ -618,16 +616,15 @@ __global__ void __launch_bounds__(norm_gate_threads<NV>(), 1)
     for (int i = 0; i < NV; ++i)
       if (in(i)) *reinterpret_cast<uint4*>(out + r * a.d + static_cast<size_t>(i * tsize + t) * E) = pack_pairs(v[i]);
   };
-  int s = 0;
+  const uint8_t* ys = ring + t * 16;
+  const uint8_t* xs = ys + 2 * static_cast<size_t>(rowbytes);
   uint32_t phase = 0;
   bool ok = true;
-  for (; row < rows; row += step) {
+  for (; row < rows; row += step, phase ^= 1) {
     const int g0 = norm_gate_group(a, row), g1 = row + 1 < rows ? norm_gate_group(a, row + 1) : -1;
-    const bool more = row + stages * step < rows;
-    const uint8_t* ys = ring + static_cast<size_t>(4 * s) * rowbytes + t * 16;
-    const uint8_t* xs = ys + 2 * static_cast<size_t>(rowbytes);
+    const bool more = row + step < rows;
     // both copies are waited for here, so that one barrier tells the team whether either gave up
-    const bool here = mbar_wait(smem_u32(&bars[team][s][0]), phase) && mbar_wait(smem_u32(&bars[team][s][1]), phase);
+    const bool here = mbar_wait(smem_u32(&bars[team][0]), phase) && mbar_wait(smem_u32(&bars[team][1]), phase);
     Row v0, v1;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -638,7 +635,7 @@ __global__ void __launch_bounds__(norm_gate_threads<NV>(), 1)
     fence_proxy_async_smem();
     ok = team_all(here);                   // and every thread has read y
     if (!ok) break;
-    if (more && t == 0) issue(s, 0, row + stages * step);
+    if (more && t == 0) issue(0, row + step);
     if (a.post_g) norm2(v0, v1, 0, true);
     if (g0 >= 0 && g0 != gs_group) load_gate(g0);
 #pragma unroll
@@ -658,7 +655,7 @@ __global__ void __launch_bounds__(norm_gate_threads<NV>(), 1)
     }
     fence_proxy_async_smem();
     team_all(true);                        // every thread has read x
-    if (more && t == 0) issue(s, 1, row + stages * step);
+    if (more && t == 0) issue(1, row + step);
     if (g0 >= 0) put(x_out, row, v0);
     if (g1 >= 0) put(x_out, row + 1, v1);
     if (a.pre_g) {
@@ -687,21 +684,12 @@ __global__ void __launch_bounds__(norm_gate_threads<NV>(), 1)
         if (g1 >= 0) put8(row + 1, v1, m1);
       }
     }
-    if (++s == stages) {
-      s = 0;
-      phase ^= 1;
-    }
   }
   // no copy may still be landing when the block exits (matters only after a timeout)
-  if (!ok)
-    for (int k = 0; k < stages && row + k * step < rows; ++k) {
-      mbar_wait(smem_u32(&bars[team][s][0]), phase);
-      mbar_wait(smem_u32(&bars[team][s][1]), phase);
-      if (++s == stages) {
-        s = 0;
-        phase ^= 1;
-      }
-    }
+  if (!ok) {
+    mbar_wait(smem_u32(&bars[team][0]), phase);
+    mbar_wait(smem_u32(&bars[team][1]), phase);
+  }
 }
 
 // fp32 rows wider than a team: one warp per row, scalar.  Only the lane that holds a column

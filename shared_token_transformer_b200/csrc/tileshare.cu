@@ -483,7 +483,7 @@ static ts_status launch_norm_gate_nv(const void* x, const void* y, void* x_out, 
     if (dev < 64) configured[dev] = 1;
   }
   // as many teams as a block's registers, shared memory and (several warps a team) named barriers hold, or as the rows
-  // give work to; then as many pairs of rows on their way as fit
+  // give work to
   constexpr int VEC = 32 * ts::Vec<T>::E * NV;    // columns of a warp
   const int team_warps = (a.d + VEC - 1) / VEC;
   const unsigned pairs = static_cast<unsigned>((static_cast<size_t>(a.rows) + 1) / 2), sms = num_sms();
@@ -492,11 +492,10 @@ static ts_status launch_norm_gate_nv(const void* x, const void* y, void* x_out, 
   teams = std::min(teams, (kNormGateSmem - vecs) / pair);
   teams = std::min<size_t>(teams, team_warps > 1 ? 15 : ts::kNormGateTeams);
   teams = std::min<size_t>(teams, (pairs + sms - 1) / sms);
-  const int stages = static_cast<int>(std::min<size_t>(ts::kNormGateStages, (kNormGateSmem - vecs) / (teams * pair)));
   trace_pre(st);
   launch_pdl(kern, dim3(std::min<unsigned>((pairs + teams - 1) / teams, sms)), dim3(32 * team_warps * teams),
-             vecs + teams * stages * pair, st, static_cast<const T*>(x), static_cast<const T*>(y), static_cast<T*>(x_out),
-             static_cast<T*>(xn), q8, qs, a, team_warps, stages);
+             vecs + teams * pair, st, static_cast<const T*>(x), static_cast<const T*>(y), static_cast<T*>(x_out),
+             static_cast<T*>(xn), q8, qs, a, team_warps);
   return trace_post(st, "norm_gate");
 }
 
