@@ -257,7 +257,7 @@ def _keep(struct, tensors):
         setattr(struct, n, t.data_ptr())
         device.add(t.get_device())
         if n.startswith("gate"):
-            groups.add(t.shape[0])
+            groups.add(t.numel() // t.shape[-1])     # a vector [d] is one group
         if n != "row_group":
             width.add(t.shape[-1])
     if len(groups) > 1 or len(width) > 1 or len(device) > 1:

@@ -1,0 +1,20 @@
+"""Which tensors the 8-bit and seam calls of the binding take: checked on host tensors, with a
+library that records calls in place of the built one, so that nothing reaches a device."""
+
+import pytest
+import torch
+
+from shared_token_transformer_b200 import binding as B
+
+
+# ---------------------------------------------------------------------------
+# descriptors of norms, gates and scales
+# ---------------------------------------------------------------------------
+def test_a_gate_given_as_a_vector_is_one_group():
+    """The kernel holds each row's group against `groups`; every group it lets through must lie in the gate."""
+    assert B.norm_gate_desc(gate=torch.zeros(64), scale=torch.zeros(64)).groups == 1
+    assert B.norm_gate_desc(gate=torch.zeros(3, 64)).groups == 3
+    sw = B.sandwich_weights(gate1=torch.zeros(1, 64), gate2=torch.zeros(64))
+    assert (sw.groups, sw.width) == (1, 64)
+    with pytest.raises(ValueError):
+        B.sandwich_weights(gate1=torch.zeros(64), gate2=torch.zeros(64, 64))
