@@ -248,12 +248,14 @@ def layer_weights(tensors):
 
 def _keep(struct, tensors):
     """Fill a struct of fp32 vectors [d], gates [groups, d] and an int32 row_group, and keep the tensors alive."""
+    import torch
     width, groups, device = set(), set(), set()
     for n, t in tensors.items():
         if t is None:
             continue
-        if not t.is_contiguous() or t.itemsize != 4:
-            raise ValueError(f"{n} must be contiguous with elements of 32 bits")
+        dtype = torch.int32 if n == "row_group" else torch.float32
+        if not t.is_contiguous() or t.dtype is not dtype:
+            raise ValueError(f"{n} must be contiguous and {dtype}")
         setattr(struct, n, t.data_ptr())
         device.add(t.get_device())
         if n.startswith("gate"):

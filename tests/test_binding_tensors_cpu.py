@@ -18,3 +18,19 @@ def test_a_gate_given_as_a_vector_is_one_group():
     assert (sw.groups, sw.width) == (1, 64)
     with pytest.raises(ValueError):
         B.sandwich_weights(gate1=torch.zeros(64), gate2=torch.zeros(64, 64))
+
+
+@pytest.mark.parametrize("name", ["post_g", "post_b", "pre_g", "pre_b", "gate", "scale"])
+def test_vectors_are_fp32(name):
+    for dtype in (torch.int32, torch.uint32, torch.float64, torch.bfloat16):
+        with pytest.raises(ValueError):
+            B.norm_gate_desc(**{name: torch.zeros(2, 64).to(dtype)})
+
+
+def test_row_groups_of_a_sandwich_are_int32():
+    for dtype in (torch.float32, torch.uint32, torch.int64):
+        with pytest.raises(ValueError):
+            B.sandwich_weights(row_group=torch.zeros(8).to(dtype))
+    with pytest.raises(ValueError):
+        B.sandwich_weights(row_group=torch.zeros(16, dtype=torch.int32)[::2])
+    assert B.sandwich_weights(row_group=torch.zeros(8, dtype=torch.int32)).row_group
