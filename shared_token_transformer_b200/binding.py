@@ -256,9 +256,12 @@ def _keep(struct, tensors):
         dtype = torch.int32 if n == "row_group" else torch.float32
         if not t.is_contiguous() or t.dtype is not dtype:
             raise ValueError(f"{n} must be contiguous and {dtype}")
+        gate = n.startswith("gate")
+        if n != "row_group" and (t.dim() == 0 or t.numel() == 0 or (t.numel() != t.shape[-1] and not gate)):
+            raise ValueError(f"{n} must be [{'groups, ' if gate else ''}d], not {list(t.shape)}")
         setattr(struct, n, t.data_ptr())
         device.add(t.get_device())
-        if n.startswith("gate"):
+        if gate:
             groups.add(t.numel() // t.shape[-1])     # a vector [d] is one group
         if n != "row_group":
             width.add(t.shape[-1])

@@ -34,3 +34,14 @@ def test_row_groups_of_a_sandwich_are_int32():
     with pytest.raises(ValueError):
         B.sandwich_weights(row_group=torch.zeros(16, dtype=torch.int32)[::2])
     assert B.sandwich_weights(row_group=torch.zeros(8, dtype=torch.int32)).row_group
+
+
+@pytest.mark.parametrize("name", ["post_g", "post_b", "pre_g", "pre_b", "gate", "scale"])
+def test_vectors_are_single_and_not_empty(name):
+    for shape in ((0,), (0, 64), (2, 0), ()):      # the address of nothing would read as "none"
+        with pytest.raises(ValueError):
+            B.norm_gate_desc(**{name: torch.zeros(shape)})
+    assert getattr(B.norm_gate_desc(**{name: torch.zeros(1, 64)}), name)
+    if name != "gate":                             # rows past the first would be left out
+        with pytest.raises(ValueError):
+            B.norm_gate_desc(**{name: torch.zeros(2, 64)})
