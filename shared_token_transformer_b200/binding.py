@@ -385,7 +385,7 @@ def quantize_rows_e4m3(x, q, scale, stream=None):
 def quantize_rows_i8(x, q, scale, stream=None):
     rows, cols = x.shape
     if not (x.is_contiguous() and q.is_contiguous() and x.nbytes == 2 * rows * cols <= 2 * q.nbytes and
-            q.itemsize == 1 and scale.nbytes >= 4 * rows and
+            q.itemsize == 1 and scale.is_contiguous() and scale.nbytes >= 4 * rows and
             x.get_device() == q.get_device() == scale.get_device() == (_device or _cuda())()):
         _unfit("ts_quantize_rows_i8")
     _check("ts_quantize_rows_i8", lib().ts_quantize_rows_i8(_ptr(x), rows, cols, _ptr(q), _ptr(scale),
@@ -417,10 +417,11 @@ def op_norm_gate(model, gates, x, y, x_out, xn=None, xn_scale=None, row_group=No
         _unfit("ts_op_norm_gate")
     if xn is not None and not (xn.is_contiguous() and xn.get_device() == device and xn.itemsize == (e if xn_scale is None else 1) and
                                xn.nbytes >= rows * d * xn.itemsize and
-                               (xn_scale is None or (xn_scale.nbytes >= 4 * rows and
+                               (xn_scale is None or (xn_scale.is_contiguous() and xn_scale.nbytes >= 4 * rows and
                                                      xn_scale.get_device() == device))):
         _unfit("ts_op_norm_gate")
-    if row_group is not None and (row_group.nbytes != 4 * rows or row_group.get_device() != device):
+    if row_group is not None and not (row_group.is_contiguous() and row_group.nbytes == 4 * rows and
+                                      row_group.get_device() == device):
         _unfit("ts_op_norm_gate")
     status = (_lib or lib()).ts_op_norm_gate(
         ctypes.byref(model), ctypes.byref(gates), x.data_ptr(), y.data_ptr(),
@@ -439,6 +440,7 @@ def op_linear(model, x, W, bias, y, epi=TS_EPI_BIAS, w_scale=None, scratch=None,
             x.nbytes == 2 * rows * K and W.nbytes == wide * K and y.nbytes >= 2 * rows * N and y.itemsize == 2 and
             w_scale is not None and scratch is not None and bias.nbytes >= 4 * wide <= w_scale.nbytes and
             scratch.nbytes >= rows * (K + 4) and x.is_contiguous() and W.is_contiguous() and y.is_contiguous() and
+            bias.is_contiguous() and w_scale.is_contiguous() and scratch.is_contiguous() and
             x.get_device() == y.get_device() == W.get_device() == bias.get_device() == w_scale.get_device() ==
             scratch.get_device() == (_device or _cuda())()):
         _unfit("ts_op_linear")
@@ -456,7 +458,8 @@ def op_linear_q8(model, x, x_scale, W, w_scale, bias, y, epi=TS_EPI_BIAS, stream
     device = (_device or _cuda())()
     if not (x.nbytes == rows * K and W.nbytes == wide * K and y.nbytes >= 2 * rows * N and y.itemsize == 2 and
             bias.nbytes >= 4 * wide <= w_scale.nbytes and x_scale.nbytes >= 4 * rows and x.is_contiguous() and
-            W.is_contiguous() and y.is_contiguous() and
+            W.is_contiguous() and y.is_contiguous() and bias.is_contiguous() and w_scale.is_contiguous() and
+            x_scale.is_contiguous() and
             x.get_device() == y.get_device() == W.get_device() == bias.get_device() == w_scale.get_device() ==
             x_scale.get_device() == device):
         _unfit("ts_op_linear_q8")

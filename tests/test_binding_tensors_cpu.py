@@ -45,3 +45,84 @@ def test_vectors_are_single_and_not_empty(name):
     if name != "gate":                             # rows past the first would be left out
         with pytest.raises(ValueError):
             B.norm_gate_desc(**{name: torch.zeros(2, 64)})
+
+
+# ---------------------------------------------------------------------------
+# tensors of the calls
+# ---------------------------------------------------------------------------
+BF, F32, I8, U8, I32 = torch.bfloat16, torch.float32, torch.int8, torch.uint8, torch.int32
+ROWS, K, N = 6, 256, 64
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Host tensors count as those of the current device, and the library notes the names of its calls."""
+    class Library:
+        def __init__(self):
+            self.names = []
+
+        def __getattr__(self, name):
+            return lambda *a: self.names.append(name) or 0
+
+    L = Library()
+    monkeypatch.setattr(torch.cuda, "init", lambda: None)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0)
+    monkeypatch.setattr(B, "_lib", L)
+    monkeypatch.setattr(B, "_device", None)
+    monkeypatch.setattr(B, "_raw_stream", None)
+    return L.names
+
+
+def model(dtype="int8"):
+    return B.model_desc(K, 4, 256, dtype, (0, 32, 32))
+
+
+def z(*shape, dtype=F32):
+    return torch.zeros(shape, dtype=dtype)
+
+
+CALLS = {
+    "quantize": (B.quantize_rows_i8, lambda: dict(x=z(ROWS, K, dtype=BF), q=z(ROWS, K, dtype=I8), scale=z(ROWS))),
+    "linear": (B.op_linear, lambda: dict(model=model(), x=z(ROWS, K, dtype=BF), W=z(N, K, dtype=I8), bias=z(N),
+                                         y=z(ROWS, N, dtype=BF), w_scale=z(N),
+                                         scratch=z(ROWS * (K + 4), dtype=U8))),
+    "linear_q8": (B.op_linear_q8, lambda: dict(model=model(), x=z(ROWS, K, dtype=I8), x_scale=z(ROWS),
+                                               W=z(N, K, dtype=I8), w_scale=z(N), bias=z(N), y=z(ROWS, N, dtype=BF))),
+    "norm_gate": (B.op_norm_gate, lambda: dict(model=model(), gates=B.norm_gate_desc(gate=z(3, K), pre_g=z(K), pre_b=z(K)),
+                                               x=z(ROWS, K, dtype=BF), y=z(ROWS, K, dtype=BF), x_out=z(ROWS, K, dtype=BF),
+                                               xn=z(ROWS, K, dtype=I8), xn_scale=z(ROWS), row_group=z(ROWS, dtype=I32))),
+}
+TENSORS = [(c, n) for c, (_, make) in CALLS.items() for n, v in make().items() if isinstance(v, torch.Tensor)]
+
+
+def refused(calls, name, **bad):
+    fn, make = CALLS[name]
+    calls.clear()
+    with pytest.raises(B.TileShareError) as e:
+        fn(**dict(make(), **bad))
+    assert e.value.status == 1 and not calls
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_tensors_that_fit_are_taken(calls, name):
+    fn, make = CALLS[name]
+    fn(**make())
+    # outputs and vectors may be longer than the call needs
+    for n, longer in (("q", z(ROWS + 1, K, dtype=I8)), ("scale", z(ROWS + 3)), ("y", z(ROWS + 2, N, dtype=BF)),
+                      ("bias", z(N + 8)), ("w_scale", z(N + 8)), ("x_scale", z(ROWS + 1)), ("scratch", z(3 * K * ROWS, dtype=U8)),
+                      ("x_out", z(ROWS + 1, K, dtype=BF)), ("xn", z(ROWS + 1, K, dtype=I8)), ("xn_scale", z(ROWS + 1)),
+                      ("q", z(ROWS * K, dtype=I8)), ("W", z(N, K, dtype=U8))):
+        if n in make() and not (n == "y" and name == "norm_gate"):
+            fn(**dict(make(), **{n: longer}))
+    assert len(calls) > 1
+
+
+@pytest.mark.parametrize("name,tensor", TENSORS)
+def test_strided_and_expanded_tensors_are_refused(calls, name, tensor):
+    """An expanded tensor counts bytes that it does not have; the elements of a strided one lie elsewhere."""
+    t = CALLS[name][1]()[tensor]
+    refused(calls, name, **{tensor: torch.zeros((1,) * t.dim(), dtype=t.dtype).expand(t.shape)})
+    every_second = torch.zeros((*t.shape, 2), dtype=t.dtype)[..., 0]
+    assert every_second.shape == t.shape
+    refused(calls, name, **{tensor: every_second})
