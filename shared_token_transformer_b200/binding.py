@@ -159,12 +159,18 @@ def _ptr(t):
 
 
 _device = _raw_stream = None      # torch's current device number, and the stream of a device as an address
+_f32 = _bf16 = _i32 = None        # torch's types
+_rows_type = _q8_types = None     # by model dtype: the type of rows, and those that 8-bit rows may have (bytes, as the
+                                  # quantisers fill them, or the type proper)
 
 
 def _cuda():
-    global _device, _raw_stream
+    global _device, _raw_stream, _f32, _bf16, _i32, _rows_type, _q8_types
     import torch
     torch.cuda.init()
+    _f32, _bf16, _i32 = torch.float32, torch.bfloat16, torch.int32
+    _rows_type = {TS_F32: _f32, TS_BF16: _bf16, TS_FP8_E4M3: _bf16, TS_INT8: _bf16}
+    _q8_types = {TS_F32: (), TS_BF16: (), TS_FP8_E4M3: (torch.float8_e4m3fn, torch.uint8), TS_INT8: (torch.int8, torch.uint8)}
     _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     return _device
 
@@ -180,9 +186,10 @@ def _stream(stream=None):
 
 
 def _unfit(fn):
-    """The 8-bit and seam calls take row-major tensors of the current device whose sizes belong together; others are
-    refused here, since a pointer does not tell."""
-    raise TileShareError(fn, 1, "a tensor is not contiguous, not on the current device, or too small for the call")
+    """quantize_rows_i8, op_linear of int8 models, op_linear_q8 and op_norm_gate take contiguous tensors of the current
+    device whose types and sizes belong together; others are refused here, since a pointer does not tell."""
+    raise TileShareError(fn, 1, "a tensor is not contiguous, of another type, not on the current device, or too small "
+                                "for the call")
 
 
 # ---------------------------------------------------------------------------
@@ -384,9 +391,10 @@ def quantize_rows_e4m3(x, q, scale, stream=None):
 
 def quantize_rows_i8(x, q, scale, stream=None):
     rows, cols = x.shape
-    if not (x.is_contiguous() and q.is_contiguous() and x.nbytes == 2 * rows * cols <= 2 * q.nbytes and
-            q.itemsize == 1 and scale.is_contiguous() and scale.nbytes >= 4 * rows and
-            x.get_device() == q.get_device() == scale.get_device() == (_device or _cuda())()):
+    device = (_device or _cuda())()
+    if not (x.dtype is _bf16 and q.dtype in _q8_types[TS_INT8] and scale.dtype is _f32 and q.nbytes >= rows * cols and
+            scale.nbytes >= 4 * rows and x.is_contiguous() and q.is_contiguous() and scale.is_contiguous() and
+            x.get_device() == q.get_device() == scale.get_device() == device):
         _unfit("ts_quantize_rows_i8")
     _check("ts_quantize_rows_i8", lib().ts_quantize_rows_i8(_ptr(x), rows, cols, _ptr(q), _ptr(scale),
                                                             _stream(stream)))
@@ -409,19 +417,22 @@ def op_layernorm(model, x, g, b, y, stream=None):
 def op_norm_gate(model, gates, x, y, x_out, xn=None, xn_scale=None, row_group=None, stream=None):
     """ts_op_norm_gate: x_out = x + gate * scale * Norm_post(y) and xn = Norm_pre(x_out), as 8-bit rows with xn_scale."""
     rows, d = x.shape
-    e = 4 if model.dtype == TS_F32 else 2
     device = (_device or _cuda())()
-    if not (d == model.d and gates.width in (d, 0) and gates.device in (device, None) and x.nbytes == y.nbytes == rows * d * e <= x_out.nbytes and
-            x_out.itemsize == e and x.is_contiguous() and y.is_contiguous() and x_out.is_contiguous() and
+    dtype = model.dtype
+    rows_type = _rows_type.get(dtype)
+    if not (x.dtype is y.dtype is x_out.dtype is rows_type and d == model.d and gates.width in (d, 0) and
+            gates.device in (device, None) and x.nbytes == y.nbytes <= x_out.nbytes and x.is_contiguous() and
+            y.is_contiguous() and x_out.is_contiguous() and
             x.get_device() == y.get_device() == x_out.get_device() == device):
         _unfit("ts_op_norm_gate")
-    if xn is not None and not (xn.is_contiguous() and xn.get_device() == device and xn.itemsize == (e if xn_scale is None else 1) and
-                               xn.nbytes >= rows * d * xn.itemsize and
-                               (xn_scale is None or (xn_scale.is_contiguous() and xn_scale.nbytes >= 4 * rows and
-                                                     xn_scale.get_device() == device))):
+    if xn is not None and not (
+            xn.is_contiguous() and xn.get_device() == device and xn.numel() >= rows * d and
+            (xn.dtype is rows_type if xn_scale is None else
+             xn.dtype in _q8_types[dtype] and xn_scale.dtype is _f32 and xn_scale.is_contiguous() and
+             xn_scale.nbytes >= 4 * rows and xn_scale.get_device() == device)):
         _unfit("ts_op_norm_gate")
-    if row_group is not None and not (row_group.is_contiguous() and row_group.nbytes == 4 * rows and
-                                      row_group.get_device() == device):
+    if row_group is not None and not (row_group.dtype is _i32 and row_group.is_contiguous() and
+                                      row_group.numel() == rows and row_group.get_device() == device):
         _unfit("ts_op_norm_gate")
     status = (_lib or lib()).ts_op_norm_gate(
         ctypes.byref(model), ctypes.byref(gates), x.data_ptr(), y.data_ptr(),
@@ -436,14 +447,16 @@ def op_linear(model, x, W, bias, y, epi=TS_EPI_BIAS, w_scale=None, scratch=None,
     rows, K = x.shape
     wide = W.shape[0]
     N = wide // 2 if epi == TS_EPI_BIAS_SWIGLU else wide     # output width
-    if model.dtype == TS_INT8 and not (
-            x.nbytes == 2 * rows * K and W.nbytes == wide * K and y.nbytes >= 2 * rows * N and y.itemsize == 2 and
-            w_scale is not None and scratch is not None and bias.nbytes >= 4 * wide <= w_scale.nbytes and
-            scratch.nbytes >= rows * (K + 4) and x.is_contiguous() and W.is_contiguous() and y.is_contiguous() and
-            bias.is_contiguous() and w_scale.is_contiguous() and scratch.is_contiguous() and
-            x.get_device() == y.get_device() == W.get_device() == bias.get_device() == w_scale.get_device() ==
-            scratch.get_device() == (_device or _cuda())()):
-        _unfit("ts_op_linear")
+    if model.dtype == TS_INT8:
+        device = (_device or _cuda())()
+        if not (w_scale is not None and scratch is not None and x.dtype is y.dtype is _bf16 and
+                W.dtype in _q8_types[TS_INT8] and bias.dtype is w_scale.dtype is _f32 and W.nbytes == wide * K and
+                y.nbytes >= 2 * rows * N and bias.nbytes >= 4 * wide <= w_scale.nbytes and
+                scratch.nbytes >= rows * (K + 4) and x.is_contiguous() and W.is_contiguous() and y.is_contiguous() and
+                bias.is_contiguous() and w_scale.is_contiguous() and scratch.is_contiguous() and
+                x.get_device() == y.get_device() == W.get_device() == bias.get_device() == w_scale.get_device() ==
+                scratch.get_device() == device):
+            _unfit("ts_op_linear")
     status = (_lib or lib()).ts_op_linear(ctypes.byref(model), x.data_ptr(), rows, K, W.data_ptr(), _ptr(w_scale), N,
                                           _ptr(bias), epi, y.data_ptr(), _ptr(scratch), _stream(stream))
     if status:
@@ -456,8 +469,10 @@ def op_linear_q8(model, x, x_scale, W, w_scale, bias, y, epi=TS_EPI_BIAS, stream
     wide = W.shape[0]
     N = wide // 2 if epi == TS_EPI_BIAS_SWIGLU else wide     # output width
     device = (_device or _cuda())()
-    if not (x.nbytes == rows * K and W.nbytes == wide * K and y.nbytes >= 2 * rows * N and y.itemsize == 2 and
-            bias.nbytes >= 4 * wide <= w_scale.nbytes and x_scale.nbytes >= 4 * rows and x.is_contiguous() and
+    q8 = _q8_types.get(model.dtype, ())
+    if not (x.dtype in q8 and W.dtype in q8 and y.dtype is _bf16 and x_scale.dtype is w_scale.dtype is bias.dtype is _f32 and
+            W.nbytes == wide * K and y.nbytes >= 2 * rows * N and bias.nbytes >= 4 * wide <= w_scale.nbytes and
+            x_scale.nbytes >= 4 * rows and x.is_contiguous() and
             W.is_contiguous() and y.is_contiguous() and bias.is_contiguous() and w_scale.is_contiguous() and
             x_scale.is_contiguous() and
             x.get_device() == y.get_device() == W.get_device() == bias.get_device() == w_scale.get_device() ==

@@ -126,3 +126,48 @@ def test_strided_and_expanded_tensors_are_refused(calls, name, tensor):
     every_second = torch.zeros((*t.shape, 2), dtype=t.dtype)[..., 0]
     assert every_second.shape == t.shape
     refused(calls, name, **{tensor: every_second})
+
+
+@pytest.mark.parametrize("name,tensor", [t for t in TENSORS if t[1] != "scratch"])
+def test_other_element_types_are_refused(calls, name, tensor):
+    """Also those of the same size: their bits would be read as the type of the call."""
+    t = CALLS[name][1]()[tensor]
+    same = {1: (torch.bool, torch.float8_e4m3fn, torch.float8_e5m2), 2: (torch.float16, torch.int16),
+            4: (torch.int32, torch.float32, torch.uint32)}[t.element_size()]
+    for dtype in (*same, torch.float64, torch.int64):
+        if dtype is not t.dtype:
+            refused(calls, name, **{tensor: torch.zeros(t.shape, dtype=torch.uint8).to(dtype)})
+    # as many bytes of a type twice as wide
+    refused(calls, name, **{tensor: torch.zeros(t.numel() // 2, dtype=torch.float64).reshape(-1, *t.shape[1:])
+                            if t.dim() == 1 else torch.zeros((t.shape[0], t.shape[1] // 2), dtype=torch.float64)})
+
+
+def test_types_of_8_bit_rows_belong_to_the_model(calls):
+    """Bytes as the quantisers fill them, or the type that the model computes in."""
+    fn, make = CALLS["linear_q8"]
+    e4m3, i8, u8 = (lambda n, t=t: z(n, K, dtype=t) for t in (torch.float8_e4m3fn, I8, U8))
+    for dtype, own, other in (("int8", i8, e4m3), ("fp8", e4m3, i8)):
+        for x, w in ((own, own), (u8, own), (own, u8), (u8, u8)):
+            fn(**dict(make(), model=model(dtype), x=x(ROWS), W=w(N)))
+        for x, w in ((other, own), (own, other)):
+            with pytest.raises(B.TileShareError):
+                fn(**dict(make(), model=model(dtype), x=x(ROWS), W=w(N)))
+    fn, make = CALLS["norm_gate"]
+    for dtype, own, other in (("int8", i8, e4m3), ("fp8", e4m3, i8)):
+        fn(**dict(make(), model=model(dtype), xn=own(ROWS)))
+        fn(**dict(make(), model=model(dtype), xn=u8(ROWS)))
+        with pytest.raises(B.TileShareError):
+            fn(**dict(make(), model=model(dtype), xn=other(ROWS)))
+    fn(**dict(make(), model=model("bf16"), xn=z(ROWS, K, dtype=BF), xn_scale=None))
+    for dtype in (torch.float16, torch.int16):
+        refused(calls, "norm_gate", xn=z(ROWS, K, dtype=dtype), xn_scale=None)
+    f32 = {n: z(ROWS, K) for n in ("x", "y", "x_out", "xn")}
+    fn(**dict(make(), model=model("f32"), xn_scale=None, **f32))
+    refused(calls, "norm_gate", **dict(f32, model=model("bf16"), xn_scale=None))
+    refused(calls, "norm_gate", model=model("f32"), xn_scale=None, **dict(f32, y=z(ROWS, K, dtype=I32)))
+
+
+def test_unknown_model_dtypes_are_refused(calls):
+    refused(calls, "norm_gate", model=model(9))
+    refused(calls, "linear_q8", model=model(9))
+    refused(calls, "linear_q8", model=model("bf16"))
