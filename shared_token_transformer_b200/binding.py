@@ -188,8 +188,13 @@ def _stream(stream=None):
 def _unfit(fn):
     """quantize_rows_i8, op_linear of int8 models, op_linear_q8 and op_norm_gate take contiguous tensors of the current
     device whose types and sizes belong together; others are refused here, since a pointer does not tell."""
-    raise TileShareError(fn, 1, "a tensor is not contiguous, of another type, not on the current device, or too small "
-                                "for the call")
+    raise TileShareError(fn, 1, "a tensor is not contiguous, of another type or shape, not on the current device, or too "
+                                "small for the call")
+
+
+def _holds(t, rows, cols):
+    """Whether the contiguous t holds the rows one behind the other: [>= rows, cols], or flat."""
+    return t.numel() >= rows * cols and t.dim() > 0 and (t.shape[-1] == cols or t.dim() == 1)
 
 
 # ---------------------------------------------------------------------------
@@ -392,8 +397,9 @@ def quantize_rows_e4m3(x, q, scale, stream=None):
 def quantize_rows_i8(x, q, scale, stream=None):
     rows, cols = x.shape
     device = (_device or _cuda())()
-    if not (x.dtype is _bf16 and q.dtype in _q8_types[TS_INT8] and scale.dtype is _f32 and q.nbytes >= rows * cols and
-            scale.nbytes >= 4 * rows and x.is_contiguous() and q.is_contiguous() and scale.is_contiguous() and
+    if not (x.dtype is _bf16 and q.dtype in _q8_types[TS_INT8] and scale.dtype is _f32 and
+            (q.shape == x.shape or _holds(q, rows, cols)) and scale.nbytes >= 4 * rows and
+            x.is_contiguous() and q.is_contiguous() and scale.is_contiguous() and
             x.get_device() == q.get_device() == scale.get_device() == device):
         _unfit("ts_quantize_rows_i8")
     _check("ts_quantize_rows_i8", lib().ts_quantize_rows_i8(_ptr(x), rows, cols, _ptr(q), _ptr(scale),
@@ -416,17 +422,20 @@ def op_layernorm(model, x, g, b, y, stream=None):
 
 def op_norm_gate(model, gates, x, y, x_out, xn=None, xn_scale=None, row_group=None, stream=None):
     """ts_op_norm_gate: x_out = x + gate * scale * Norm_post(y) and xn = Norm_pre(x_out), as 8-bit rows with xn_scale."""
-    rows, d = x.shape
+    shape = x.shape
+    rows, d = shape
     device = (_device or _cuda())()
     dtype = model.dtype
     rows_type = _rows_type.get(dtype)
-    if not (x.dtype is y.dtype is x_out.dtype is rows_type and d == model.d and gates.width in (d, 0) and
-            gates.device in (device, None) and x.nbytes == y.nbytes <= x_out.nbytes and x.is_contiguous() and
-            y.is_contiguous() and x_out.is_contiguous() and
+    if not (x.dtype is y.dtype is x_out.dtype is rows_type and d == model.d and (gates.width == d or gates.width == 0) and
+            (gates.device == device or gates.device is None) and
+            (shape == y.shape or (y.numel() == rows * d and _holds(y, rows, d))) and
+            (shape == x_out.shape or _holds(x_out, rows, d)) and
+            x.is_contiguous() and y.is_contiguous() and x_out.is_contiguous() and
             x.get_device() == y.get_device() == x_out.get_device() == device):
         _unfit("ts_op_norm_gate")
     if xn is not None and not (
-            xn.is_contiguous() and xn.get_device() == device and xn.numel() >= rows * d and
+            xn.is_contiguous() and xn.get_device() == device and (shape == xn.shape or _holds(xn, rows, d)) and
             (xn.dtype is rows_type if xn_scale is None else
              xn.dtype in _q8_types[dtype] and xn_scale.dtype is _f32 and xn_scale.is_contiguous() and
              xn_scale.nbytes >= 4 * rows and xn_scale.get_device() == device)):
@@ -451,7 +460,7 @@ def op_linear(model, x, W, bias, y, epi=TS_EPI_BIAS, w_scale=None, scratch=None,
         device = (_device or _cuda())()
         if not (w_scale is not None and scratch is not None and x.dtype is y.dtype is _bf16 and
                 W.dtype in _q8_types[TS_INT8] and bias.dtype is w_scale.dtype is _f32 and W.nbytes == wide * K and
-                y.nbytes >= 2 * rows * N and bias.nbytes >= 4 * wide <= w_scale.nbytes and
+                (y.shape == (rows, N) or _holds(y, rows, N)) and bias.nbytes >= 4 * wide <= w_scale.nbytes and
                 scratch.nbytes >= rows * (K + 4) and x.is_contiguous() and W.is_contiguous() and y.is_contiguous() and
                 bias.is_contiguous() and w_scale.is_contiguous() and scratch.is_contiguous() and
                 x.get_device() == y.get_device() == W.get_device() == bias.get_device() == w_scale.get_device() ==
@@ -471,8 +480,8 @@ def op_linear_q8(model, x, x_scale, W, w_scale, bias, y, epi=TS_EPI_BIAS, stream
     device = (_device or _cuda())()
     q8 = _q8_types.get(model.dtype, ())
     if not (x.dtype in q8 and W.dtype in q8 and y.dtype is _bf16 and x_scale.dtype is w_scale.dtype is bias.dtype is _f32 and
-            W.nbytes == wide * K and y.nbytes >= 2 * rows * N and bias.nbytes >= 4 * wide <= w_scale.nbytes and
-            x_scale.nbytes >= 4 * rows and x.is_contiguous() and
+            W.nbytes == wide * K and (y.shape == (rows, N) or _holds(y, rows, N)) and
+            bias.nbytes >= 4 * wide <= w_scale.nbytes and x_scale.nbytes >= 4 * rows and x.is_contiguous() and
             W.is_contiguous() and y.is_contiguous() and bias.is_contiguous() and w_scale.is_contiguous() and
             x_scale.is_contiguous() and
             x.get_device() == y.get_device() == W.get_device() == bias.get_device() == w_scale.get_device() ==

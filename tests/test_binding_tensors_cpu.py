@@ -171,3 +171,16 @@ def test_unknown_model_dtypes_are_refused(calls):
     refused(calls, "norm_gate", model=model(9))
     refused(calls, "linear_q8", model=model(9))
     refused(calls, "linear_q8", model=model("bf16"))
+
+
+@pytest.mark.parametrize("name,tensor", [("quantize", "q"), ("linear", "y"), ("linear_q8", "y"), ("norm_gate", "y"),
+                                         ("norm_gate", "x_out"), ("norm_gate", "xn")])
+def test_rows_of_another_length_are_refused(calls, name, tensor):
+    """Outputs are written row after row: one with longer rows, or with its sides exchanged, would be scrambled."""
+    t = CALLS[name][1]()[tensor]
+    rows, cols = t.shape
+    for shape in ((rows, cols + 8), (2 * rows, cols // 2), (cols, rows), (rows, cols, 1)):
+        refused(calls, name, **{tensor: torch.zeros(shape, dtype=t.dtype)})
+    fn, make = CALLS[name]
+    fn(**dict(make(), **{tensor: t.reshape(-1)}))                 # the same elements in one dimension
+    fn(**dict(make(), **{tensor: t.reshape(2, rows // 2, cols)}))
