@@ -114,12 +114,12 @@ _SIGS = {
                                  ctypes.POINTER(SandwichWeights), _cp, _cp, ctypes.c_size_t, _cp],
     "ts_block_tiled_sandwich": [_cp, ctypes.POINTER(ModelDesc), ctypes.POINTER(LayerWeights),
                                 ctypes.POINTER(SandwichWeights), _cp, _cp, ctypes.c_size_t, _cp],
-    "ts_op_norm_gate": [ctypes.POINTER(ModelDesc), ctypes.POINTER(NormGate), _cp, _cp, _cp, ctypes.c_int, _cp, _cp,
+    "ts_op_norm_gate": [_cp, ctypes.POINTER(NormGate), _cp, _cp, _cp, ctypes.c_int, _cp, _cp,
                         _cp, _cp],
     "ts_op_layernorm": [ctypes.POINTER(ModelDesc), _cp, ctypes.c_int, _cp, _cp, _cp, _cp],
-    "ts_op_linear": [ctypes.POINTER(ModelDesc), _cp, ctypes.c_int, ctypes.c_int, _cp, _cp, ctypes.c_int, _cp,
+    "ts_op_linear": [_cp, _cp, ctypes.c_int, ctypes.c_int, _cp, _cp, ctypes.c_int, _cp,
                      ctypes.c_int, _cp, _cp, _cp],
-    "ts_op_linear_q8": [ctypes.POINTER(ModelDesc), _cp, _cp, ctypes.c_int, ctypes.c_int, _cp, _cp, ctypes.c_int, _cp,
+    "ts_op_linear_q8": [_cp, _cp, _cp, ctypes.c_int, ctypes.c_int, _cp, _cp, ctypes.c_int, _cp,
                         ctypes.c_int, _cp, _cp],
     "ts_op_qkv": [_cp, ctypes.POINTER(ModelDesc), ctypes.POINTER(LayerWeights), ctypes.c_int, _cp, _cp, _cp, _cp],
     "ts_op_attention": [_cp, ctypes.POINTER(ModelDesc), ctypes.c_int, _cp, _cp, _cp],
@@ -444,7 +444,7 @@ def op_norm_gate(model, gates, x, y, x_out, xn=None, xn_scale=None, row_group=No
                                       row_group.numel() == rows and row_group.get_device() == device):
         _unfit("ts_op_norm_gate")
     status = (_lib or lib()).ts_op_norm_gate(
-        ctypes.byref(model), ctypes.byref(gates), x.data_ptr(), y.data_ptr(),
+        ctypes.addressof(model), gates, x.data_ptr(), y.data_ptr(),
         None if row_group is None else row_group.data_ptr(), rows, x_out.data_ptr(),
         None if xn is None else xn.data_ptr(), None if xn_scale is None else xn_scale.data_ptr(),
         _raw_stream(device) if stream is None else stream.cuda_stream)
@@ -466,8 +466,10 @@ def op_linear(model, x, W, bias, y, epi=TS_EPI_BIAS, w_scale=None, scratch=None,
                 x.get_device() == y.get_device() == W.get_device() == bias.get_device() == w_scale.get_device() ==
                 scratch.get_device() == device):
             _unfit("ts_op_linear")
-    status = (_lib or lib()).ts_op_linear(ctypes.byref(model), x.data_ptr(), rows, K, W.data_ptr(), _ptr(w_scale), N,
-                                          _ptr(bias), epi, y.data_ptr(), _ptr(scratch), _stream(stream))
+    status = (_lib or lib()).ts_op_linear(ctypes.addressof(model), x.data_ptr(), rows, K, W.data_ptr(),
+                                          None if w_scale is None else w_scale.data_ptr(), N,
+                                          None if bias is None else bias.data_ptr(), epi, y.data_ptr(),
+                                          None if scratch is None else scratch.data_ptr(), _stream(stream))
     if status:
         _check("ts_op_linear", status)
 
@@ -487,7 +489,7 @@ def op_linear_q8(model, x, x_scale, W, w_scale, bias, y, epi=TS_EPI_BIAS, stream
             x.get_device() == y.get_device() == W.get_device() == bias.get_device() == w_scale.get_device() ==
             x_scale.get_device() == device):
         _unfit("ts_op_linear_q8")
-    status = (_lib or lib()).ts_op_linear_q8(ctypes.byref(model), x.data_ptr(), x_scale.data_ptr(), rows, K,
+    status = (_lib or lib()).ts_op_linear_q8(ctypes.addressof(model), x.data_ptr(), x_scale.data_ptr(), rows, K,
                                              W.data_ptr(), w_scale.data_ptr(), N, bias.data_ptr(), epi, y.data_ptr(),
                                              _raw_stream(device) if stream is None else stream.cuda_stream)
     if status:
