@@ -458,8 +458,8 @@ def op_linear(model, x, W, bias, y, epi=TS_EPI_BIAS, w_scale=None, scratch=None,
     N = wide // 2 if epi == TS_EPI_BIAS_SWIGLU else wide     # output width
     if model.dtype == TS_INT8:
         device = (_device or _cuda())()
-        if not (w_scale is not None and scratch is not None and x.dtype is y.dtype is _bf16 and
-                W.dtype in _q8_types[TS_INT8] and bias.dtype is w_scale.dtype is _f32 and W.nbytes == wide * K and
+        if not (bias is not None and y is not None and w_scale is not None and scratch is not None and
+                x.dtype is y.dtype is _bf16 and W.dtype in _q8_types[TS_INT8] and bias.dtype is w_scale.dtype is _f32 and W.nbytes == wide * K and
                 (y.shape == (rows, N) or _holds(y, rows, N)) and bias.nbytes >= 4 * wide <= w_scale.nbytes and
                 scratch.nbytes >= rows * (K + 4) and x.is_contiguous() and W.is_contiguous() and y.is_contiguous() and
                 bias.is_contiguous() and w_scale.is_contiguous() and scratch.is_contiguous() and
@@ -468,7 +468,8 @@ def op_linear(model, x, W, bias, y, epi=TS_EPI_BIAS, w_scale=None, scratch=None,
             _unfit("ts_op_linear")
     status = (_lib or lib()).ts_op_linear(ctypes.addressof(model), x.data_ptr(), rows, K, W.data_ptr(),
                                           None if w_scale is None else w_scale.data_ptr(), N,
-                                          None if bias is None else bias.data_ptr(), epi, y.data_ptr(),
+                                          None if bias is None else bias.data_ptr(), epi,
+                                          None if y is None else y.data_ptr(),
                                           None if scratch is None else scratch.data_ptr(), _stream(stream))
     if status:
         _check("ts_op_linear", status)

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from shared_token_transformer_b200 import binding as B
+from shared_token_transformer_b200 import build as Bd
 
 
 # ---------------------------------------------------------------------------
@@ -184,3 +185,15 @@ def test_rows_of_another_length_are_refused(calls, name, tensor):
     fn, make = CALLS[name]
     fn(**dict(make(), **{tensor: t.reshape(-1)}))                 # the same elements in one dimension
     fn(**dict(make(), **{tensor: t.reshape(2, rows // 2, cols)}))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8", "int8"])
+@pytest.mark.parametrize("missing", ["y", "bias"])
+def test_a_missing_tensor_of_a_linear_layer_is_an_error_of_the_call(calls, monkeypatch, dtype, missing):
+    Bd.build()
+    monkeypatch.setattr(B, "_lib", None)              # the library itself, which refuses it before anything runs
+    args = CALLS["linear"][1]()
+    args["model"] = B.model_desc(64, 4, 256, dtype, (0, 8, 8)) if dtype == "f32" else model(dtype)
+    with pytest.raises(B.TileShareError) as e:
+        B.op_linear(**dict(args, **{missing: None}))
+    assert e.value.status == 1
