@@ -1881,17 +1881,18 @@ ts_status ts_op_linear(const ts_model_desc* m, const void* x, int rows, int K, c
   if (m->dtype == TS_F32)
     return run_gemm_f32("linear", e, static_cast<const float*>(x), static_cast<const float*>(W), rows, N, K, bias,
                         static_cast<float*>(y), st);
+  if (has_q8(m) && ((rows && !scratch) || !aligned16(scratch) || !w_scale || !aligned16(w_scale)))
+    return fail(TS_ERR_INVALID_ARG, "8-bit linear needs scratch and w_scale, 16-byte aligned");
+  if (rows == 0) return TS_OK;
   TS_TRY(check_gemm_sizes(m, K, N));
   if (has_q8(m)) {
-    if ((rows && !scratch) || !aligned16(scratch) || !w_scale || !aligned16(w_scale))
-      return fail(TS_ERR_INVALID_ARG, "8-bit linear needs scratch and w_scale, 16-byte aligned");
     uint8_t* q8 = static_cast<uint8_t*>(scratch);
     float* qs = reinterpret_cast<float*>(q8 + static_cast<size_t>(rows) * K);   // K % 16 == 0 keeps it aligned
     // A few rows and a W of at most 8 MB: one launch, in which the blocks quantise the rows.  1 x 1536 -> 4608 then takes
     // 5.2 us a call from a stream against 7.4 by two launches (3.9 against 3.0 in a graph), 1 x 512 -> 2048 in a graph
     // 2.1 against 2.6; with more of W the two win everywhere (6 x 6144 -> 1536 in a graph 6.0 against 8.8).
     const double w_bytes = static_cast<double>(e == ts::EPI_SWIGLU ? 2 * N : N) * K;
-    if (m->dtype == TS_INT8 && rows > 0 && rows <= 8 && K <= 2048 && w_bytes <= 8.0 * (1 << 20)) {
+    if (m->dtype == TS_INT8 && rows <= 8 && K <= 2048 && w_bytes <= 8.0 * (1 << 20)) {
       set_linear_work("linear", m, e, rows, N, K, 2.0);
       return run_gemm_s8_few(e, nullptr, nullptr, static_cast<const bf16*>(x), W, w_scale, rows, N, K, bias,
                              static_cast<bf16*>(y), false, st);
@@ -1913,6 +1914,7 @@ ts_status ts_op_linear_q8(const ts_model_desc* m, const void* x, const float* x_
     return fail(TS_ERR_INVALID_ARG, "alignment");
   int e = 0;
   TS_TRY(epilogue_of(epi, &e));
+  if (rows == 0) return TS_OK;
   TS_TRY(check_gemm_sizes(m, K, N));
   return run_gemm_tc("linear", m, e, x, x_scale, W, w_scale, rows, N, K, bias, static_cast<bf16*>(y), nullptr, nullptr,
                      static_cast<cudaStream_t>(stream));
