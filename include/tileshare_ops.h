@@ -69,6 +69,8 @@ ts_status ts_op_norm_gate(const ts_model_desc* model, const ts_norm_gate* p, con
    rows * K + 4 * rows bytes and belongs to the call until it has run: calls in flight
    at once, captured graphs among them, need one each; scratch is unused otherwise and
    may be NULL).
+   8-bit dtypes: y may lie over x, as the rows are quantised first; else x and y must not
+   overlap.
    bf16/e4m3 need K % 64 == 0 and N % 64 == 0 (K % 128 for e4m3); int8 needs
    K % 16 == 0, N % 8 == 0 and K <= 131056. */
 ts_status ts_op_linear(const ts_model_desc* model, const void* x, int rows, int K,
@@ -78,7 +80,7 @@ ts_status ts_op_linear(const ts_model_desc* model, const void* x, int rows, int 
 /* The same linear layer of rows that are 8-bit already (8-bit dtypes only): x [rows, K]
    e4m3 or signed bytes with x_scale [rows], as ts_quantize_rows_* and ts_op_norm_gate
    write them; y = epi((x W^T) * x_scale * w_scale + b), y bf16 [rows, N].  Integer sums
-   are exact.  x may hold -128.  Sizes as for ts_op_linear. */
+   are exact.  x may hold -128.  Sizes as for ts_op_linear; y must not overlap x. */
 ts_status ts_op_linear_q8(const ts_model_desc* model, const void* x, const float* x_scale,
                           int rows, int K, const void* W, const float* w_scale, int N,
                           const float* bias, ts_epilogue epi, void* y, void* stream);

@@ -67,6 +67,11 @@ static ts_status fail(ts_status s, const char* fmt, ...) {
 
 static inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+static inline bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return p < q + b_bytes && q < p + a_bytes;
+}
+
 static ts_status launched(const char* what) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(TS_ERR_CUDA, "launch of %s failed: %s", what, cudaGetErrorString(e));
@@ -1891,8 +1896,10 @@ ts_status ts_op_linear(const ts_model_desc* m, const void* x, int rows, int K, c
     // A few rows and a W of at most 8 MB: one launch, in which the blocks quantise the rows.  1 x 1536 -> 4608 then takes
     // 5.2 us a call from a stream against 7.4 by two launches (3.9 against 3.0 in a graph), 1 x 512 -> 2048 in a graph
     // 2.1 against 2.6; with more of W the two win everywhere (6 x 6144 -> 1536 in a graph 6.0 against 8.8).
+    // (not where y lies over x: its blocks read all rows while others write)
     const double w_bytes = static_cast<double>(e == ts::EPI_SWIGLU ? 2 * N : N) * K;
-    if (m->dtype == TS_INT8 && rows <= 8 && K <= 2048 && w_bytes <= 8.0 * (1 << 20)) {
+    const size_t r = static_cast<size_t>(rows);
+    if (m->dtype == TS_INT8 && rows <= 8 && K <= 2048 && w_bytes <= 8.0 * (1 << 20) && !overlap(x, r * K * 2, y, r * N * 2)) {
       set_linear_work("linear", m, e, rows, N, K, 2.0);
       return run_gemm_s8_few(e, nullptr, nullptr, static_cast<const bf16*>(x), W, w_scale, rows, N, K, bias,
                              static_cast<bf16*>(y), false, st);
@@ -1916,6 +1923,8 @@ ts_status ts_op_linear_q8(const ts_model_desc* m, const void* x, const float* x_
   TS_TRY(epilogue_of(epi, &e));
   if (rows == 0) return TS_OK;
   TS_TRY(check_gemm_sizes(m, K, N));
+  const size_t r = static_cast<size_t>(rows);
+  if (overlap(x, r * K, y, r * N * 2)) return fail(TS_ERR_INVALID_ARG, "y and x overlap");
   return run_gemm_tc("linear", m, e, x, x_scale, W, w_scale, rows, N, K, bias, static_cast<bf16*>(y), nullptr, nullptr,
                      static_cast<cudaStream_t>(stream));
 }

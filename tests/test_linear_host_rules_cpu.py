@@ -33,3 +33,13 @@ def test_no_rows_are_no_work_at_any_size(dtype):
         assert linear(dtype, 0, K, N) == 0
         if dtype in ("fp8", "int8"):
             assert linear_q8(dtype, 0, K, N) == 0
+
+
+@pytest.mark.parametrize("dtype", ["fp8", "int8"])
+def test_linear_q8_refuses_an_output_over_its_rows(dtype):
+    """Tiles are written while others still read the rows."""
+    rows, K, N = 4, 128, 64                        # x 512 bytes, y 512 bytes
+    for y in (P, P + 16, P + 496, P - 16, P - 496):
+        assert linear_q8(dtype, rows, K, N, y=y) == 1, y - P
+        assert b"overlap" in B.lib().ts_last_error()
+    assert linear_q8(dtype, 0, K, N, y=P) == 0
