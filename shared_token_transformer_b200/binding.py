@@ -466,11 +466,14 @@ def op_linear(model, x, W, bias, y, epi=TS_EPI_BIAS, w_scale=None, scratch=None,
                 x.get_device() == y.get_device() == W.get_device() == bias.get_device() == w_scale.get_device() ==
                 scratch.get_device() == device):
             _unfit("ts_op_linear")
+        st = _raw_stream(device) if stream is None else stream.cuda_stream
+    else:
+        st = _stream(stream)
     status = (_lib or lib()).ts_op_linear(ctypes.addressof(model), x.data_ptr(), rows, K, W.data_ptr(),
                                           None if w_scale is None else w_scale.data_ptr(), N,
                                           None if bias is None else bias.data_ptr(), epi,
                                           None if y is None else y.data_ptr(),
-                                          None if scratch is None else scratch.data_ptr(), _stream(stream))
+                                          None if scratch is None else scratch.data_ptr(), st)
     if status:
         _check("ts_op_linear", status)
 
