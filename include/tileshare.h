@@ -86,7 +86,7 @@ typedef enum {
   /* Norm1/Norm2 RMSNorm with gain, no bias (ln*_b unused, may be NULL); MLP
      W_2 (silu(W_g h + b_g) * (W_u h + b_u)) + b_2 with silu(z) = z / (1 + e^-z).
      w_1 [2f, d] holds the f gate rows W_g above the f up rows W_u; b_1 [2f] and, for
-     e4m3, s_1 [2f] follow the same order. */
+     the 8-bit dtypes, s_1 [2f] follow the same order. */
   TS_BLOCK_RMS_SWIGLU = 1
 } ts_block_kind;
 
@@ -176,7 +176,7 @@ ts_status ts_workspace_size(ts_plan_t plan, const ts_model_desc* model, int L, i
                             size_t* bytes);
 
 /* One released (per-tile) layer, in place on X [T, N, d] (device, model dtype; bf16
-   for TS_FP8_E4M3).  [TileShare] Tab. S1, "Layer 0" column: every tile keeps its
+   for the 8-bit dtypes).  [TileShare] Tab. S1, "Layer 0" column: every tile keeps its
    own residual stream; Norm1, QKV, QK-RMSNorm, RoPE on tile-local coordinates (the
    registers are not rotated), dense attention over the tile's N rows,
    out-projection, Norm2 and MLP per tile row. */

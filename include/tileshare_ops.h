@@ -94,7 +94,7 @@ ts_status ts_op_linear_q8(const ts_model_desc* model, const void* x, const float
    the tile's origin: attention scores then equal those of tile-local rotation
    exactly (RoPE scores depend on coordinate differences only), so the rotation
    can run once per token.  `scratch` holds, each region 256-byte aligned, the
-   normalised rows (rows * d elements of the model dtype), an e4m3 copy
+   normalised rows (rows * d elements of the model dtype), an 8-bit copy
    (rows * d bytes) with per-row scales (4 * rows bytes), and the RoPE cos/sin
    table (8 * (F * D_f + H * D_y + W * D_x) / 2 bytes). */
 ts_status ts_op_qkv(ts_plan_t plan, const ts_model_desc* model, const ts_layer_weights* w,

@@ -287,7 +287,7 @@ def _keep(struct, tensors):
 
 
 def norm_gate_desc(post_g=None, post_b=None, pre_g=None, pre_b=None, gate=None, scale=None):
-    """ts_norm_gate of device tensors (fp32; gate [groups, d]), kept alive by the struct."""
+    """ts_norm_gate of device tensors (fp32 [d]; gate [groups, d], or [d] for one group), kept alive by the struct."""
     return _keep(NormGate(), {"post_g": post_g, "post_b": post_b, "pre_g": pre_g, "pre_b": pre_b, "gate": gate,
                               "scale": scale})
 

@@ -274,9 +274,11 @@ struct RowCode {
 
 // Few rows: a block of d / E threads (E columns each) takes two rows at a time, with its
 // columns' gains, biases and gates in registers; what counts is the chain of loads and
-// reductions of one pair.  1 x 1536 takes 3.0 us against 4.2 us by norm_gate_kernel,
-// 512 x 1536 3.7 against 6.4 us; from about two pairs a block on the latter is faster
-// (4000 x 1536: 16.5 us against 20).
+// reductions of one pair.  In a graph 1 x 1536 takes 2.8 us against 6.3 by norm_gate_kernel,
+// 512 x 1536 4.0 against 6.3 us; from about two pairs a block on the latter is faster
+// (4000 x 1536: 16.7 us against 20.4).  Near the border the two lie within a fifth of each
+// other, either way (2000 x 1024 8.2 and 8.1 us, 6000 x 256 7.3 and 6.1, 2000 x 2048 14.7
+// and 16.4), as each goes up in steps of whole rounds of its grid.
 template <typename T, int Q8>
 __global__ void __launch_bounds__(256) norm_gate_few_kernel(const T* x, const T* y, T* x_out, T* xn, uint8_t* q8,
                                                             float* qscale, const NormGateArgs a) {

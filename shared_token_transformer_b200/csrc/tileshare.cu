@@ -281,13 +281,13 @@ static ts_status check_model(const ts_model_desc* m) {
     if (hd != 16 && hd != 32 && hd != 64) return fail(TS_ERR_UNSUPPORTED, "fp32 path supports head dim 16, 32, 64");
     if (m->d % 4 || m->mlp % 4) return fail(TS_ERR_UNSUPPORTED, "fp32 path needs d, mlp multiples of 4");
   } else {
-    if (hd != 64) return fail(TS_ERR_UNSUPPORTED, "bf16/e4m3 path supports head dim 64 only");
-    if (m->d % 256 || m->d > 2048) return fail(TS_ERR_UNSUPPORTED, "bf16/e4m3 path needs d %% 256 == 0, d <= 2048");
-    if (m->mlp % 256) return fail(TS_ERR_UNSUPPORTED, "bf16/e4m3 path needs mlp %% 256 == 0");
+    if (hd != 64) return fail(TS_ERR_UNSUPPORTED, "bf16 and 8-bit paths support head dim 64 only");
+    if (m->d % 256 || m->d > 2048) return fail(TS_ERR_UNSUPPORTED, "bf16 and 8-bit paths need d %% 256 == 0, d <= 2048");
+    if (m->mlp % 256) return fail(TS_ERR_UNSUPPORTED, "bf16 and 8-bit paths need mlp %% 256 == 0");
     const int* r = m->rope_dims;
     const bool s2 = r[0] == 0 && r[1] == 32 && r[2] == 32;
     const bool s3 = r[0] == 16 && r[1] == 24 && r[2] == 24;
-    if (!s2 && !s3) return fail(TS_ERR_UNSUPPORTED, "bf16/e4m3 path supports rope_dims (0,32,32) or (16,24,24)");
+    if (!s2 && !s3) return fail(TS_ERR_UNSUPPORTED, "bf16 and 8-bit paths support rope_dims (0,32,32) or (16,24,24)");
   }
   return TS_OK;
 }
