@@ -67,8 +67,8 @@ def calls(monkeypatch):
 
     L = Library()
     monkeypatch.setattr(torch.cuda, "init", lambda: None)
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1)
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
     monkeypatch.setattr(B, "_lib", L)
     monkeypatch.setattr(B, "_device", None)
     monkeypatch.setattr(B, "_raw_stream", None)
